@@ -247,7 +247,8 @@ def prepare(case, seed):
     if own:
         from post_weight_quantization_12_b200 import api
         s["cache"] = api.QuantizedCache.of_tensors(
-            s["k_codes"], s["k_scales"], s["k_zeros"], s["v_codes"], s["v_scales"], s["v_zeros"])
+            s["k_codes"], s["k_scales"], s["k_zeros"], s["v_codes"], s["v_scales"], s["v_zeros"],
+            dim=case["dim"])
     return s
 
 
