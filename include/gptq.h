@@ -65,6 +65,8 @@ typedef enum gptq_route {
 #define GPTQ_INFO_TIMEOUT (-1)        /* a bounded wait inside a kernel expired */
 #define GPTQ_INFO_BAD_HESSIAN (-2)    /* mean(diag H) <= 0 or not finite: nothing to damp */
 #define GPTQ_INFO_BAD_CODE (-3)       /* a pack call met a code too wide for its format */
+#define GPTQ_INFO_BAD_PAGE (-4)       /* a cache call met a position without a page, or a length
+                                         outside its page table */
 
 /* Which workspace gptq_workspace_size() reports. */
 #define GPTQ_WS_PREPARE 1
@@ -364,6 +366,129 @@ gptq_status gptq_obq_quantize(const float* W_dev, int64_t rows, int64_t cols, in
                               uint8_t* codes_dev, float* W_hat_dev, int32_t* order_dev,
                               double* loss_dev, float* scales_dev, uint8_t* zeros_dev,
                               void* stream);
+
+/*
+ * The quantized key/value cache of attention layers: keys and values on 4- or 8-bit grids, written
+ * as they are made, read back, and attended to without being unpacked in memory. At decode time it
+ * is the other large read beside the packed weights of gptq_w4a16_matmul.
+ *
+ * Source: "GPTQ second-order quantization" blog, "Group-wise quantization" (one scale and zero
+ * point per group) for the grid, and the W4A16 reading of gptq_w4a16_matmul (moved packed,
+ * dequantized inside the kernel) for the products. The pages have no cache; layout and grid are:
+ *
+ * A cache holds `pages` pages of `page` tokens for `heads` heads of `dim` dimensions, in
+ * caller-owned tensors, for K and V each:
+ *   codes   uint32 [pages][heads][page][dim * bits / 32]: the row of one token and head, code d in
+ *           bits bits * (d mod (32 / bits)) and up of word d / (32 / bits);
+ *   scales  bf16 (as uint16) [pages][heads][page][dim / group];
+ *   zeros   uint8 [pages][heads][page][dim / group].
+ * A group's codes q stand for s (q - z). Its grid: lo = min(0, min x), hi = max(0, max x),
+ * step = (hi - lo) / (2^bits - 1) (a step of 0 takes lo = -1, hi = 1), s = step rounded up to bf16,
+ * z = clamp(rint(-lo / s), 0, 2^bits - 1), q = clamp(rint(x / s) + z, 0, 2^bits - 1), each step
+ * rounded once in float32, half to even. A group with a value that is not finite, or whose step is
+ * not, gets a NaN scale and zero codes: it reads back as NaN.
+ *
+ * gptq_cache: dim 64 or 128; bits 4 or 8; group 32, 64 or 128, dividing dim; page a power of two
+ * from 16 to 32768; all six tensors 16-byte aligned and distinct.
+ *
+ * gptq_cache_rows: the rows of a call and where they sit. Position p of sequence b is token
+ * p % page of page table[b * ld_table + p / page]. Rows starts[b] .. starts[b + 1] - 1 belong to
+ * sequence b and are its last positions: row i is position lengths[b] - starts[b + 1] + i, so the
+ * last one is lengths[b] - 1. starts (batch + 1 values, the first 0, ascending) may be NULL: one
+ * row per sequence, n <= batch. Rows from starts[batch] on are ignored: outputs of theirs are left
+ * as they were. Everything here lives on the device and may change between replays of a graph.
+ * lengths must not exceed width * page. A page number outside 0 .. pages - 1 and a position past
+ * the table are found by the kernels, which set GPTQ_INFO_BAD_PAGE and leave the position out.
+ */
+typedef struct gptq_cache {
+  uint32_t* k_codes_dev;
+  uint16_t* k_scales_dev;
+  uint8_t* k_zeros_dev;
+  uint32_t* v_codes_dev;
+  uint16_t* v_scales_dev;
+  uint8_t* v_zeros_dev;
+  int64_t pages;
+  int heads, page, dim, bits, group;
+} gptq_cache;
+
+typedef struct gptq_cache_rows {
+  const int32_t* table_dev;    /* [batch][ld_table], columns 0 .. width - 1 used */
+  int64_t ld_table;
+  int width;
+  const int32_t* lengths_dev;  /* [batch], the new rows included */
+  const int32_t* starts_dev;   /* [batch + 1] or NULL */
+  int64_t batch;
+  int64_t n;                   /* rows of the call's tensors */
+} gptq_cache_rows;
+
+/*
+ * Quantizes n rows of keys and values into their positions.
+ *   K_dev, V_dev  [n][heads * dim] GPTQ_BF16 or GPTQ_FP32, row strides ldk, ldv (elements), 16-byte
+ *                 aligned rows.
+ *   K_hat_dev, V_hat_dev  [n][heads * dim] dense, of the same type, or NULL: what the codes stand
+ *                 for, s (q - z) (rounded to nearest even for bf16), of the rows that were stored.
+ * Two rows of one call must not share a position (sequences that share a page may not write into
+ * it): which codes and which grid remain is then not determined.
+ * n == 0 enqueues nothing. Errors: GPTQ_EINVAL (shapes, null pointers, alignment, dtype),
+ * GPTQ_EUNSUPPORTED (dim, bits, group or page that the library does not implement; more than 2^40
+ * values).
+ */
+gptq_status gptq_cache_append(const gptq_cache* cache, const gptq_cache_rows* rows,
+                              const void* K_dev, int64_t ldk, const void* V_dev, int64_t ldv,
+                              gptq_dtype dtype, void* K_hat_dev, void* V_hat_dev,
+                              int32_t* info_dev, void* stream);
+
+/*
+ * Reads the positions of n rows back: K_out_dev, V_out_dev [n][heads * dim] dense, GPTQ_BF16
+ * (rounded to nearest even) or GPTQ_FP32 (exact); one of them may be NULL. A whole sequence is read
+ * with as many rows as it is long. A position without a page reads as 0. Errors as
+ * gptq_cache_append.
+ */
+gptq_status gptq_cache_read(const gptq_cache* cache, const gptq_cache_rows* rows, void* K_out_dev,
+                            void* V_out_dev, gptq_dtype dtype, int32_t* info_dev, void* stream);
+
+/*
+ * Attention of n rows of queries, one or several tokens per sequence, over the cache:
+ *   out[i][h] = sum_t w_t v_t / sum_t w_t,  w_t = exp(scale * q[i][h] . k_t),
+ * t over the positions up to the row's own (causal), k and v of cache head h / ratio. A row that
+ * meets no position gives 0.
+ *   Q_dev, out_dev  [n][heads * ratio * dim] bf16, row strides ldq, ldo (elements, multiples of 8),
+ *                   16-byte aligned; they must not overlap.
+ *   ratio           query heads per cache head, 1 .. 1024.
+ *   scale           usually 1 / sqrt(dim); finite.
+ *   ws_dev          gptq_cache_workspace_size(cache, n, ratio, 0) bytes, 256-byte aligned; calls
+ *                   that may overlap on the GPU need one each, graphs captured with the same one
+ *                   must not be replayed at the same time.
+ * Arithmetic: products of fp16 operands with fp32 sums. Codes are exact; the weights are rounded to
+ * fp16 (2^-12 of each) relative to the largest, fp32 otherwise; one rounding to bf16 at the end.
+ * V scales below 2^-96 lose accuracy relative to themselves. Results do not depend on timing, and
+ * are the same again for the same call on the same device.
+ * n == 0 enqueues nothing. Errors: as gptq_cache_append, GPTQ_EWORKSPACE.
+ */
+gptq_status gptq_cache_attend(const gptq_cache* cache, const gptq_cache_rows* rows,
+                              const void* Q_dev, int64_t ldq, int ratio, float scale, void* out_dev,
+                              int64_t ldo, void* ws_dev, size_t ws_bytes, int32_t* info_dev,
+                              void* stream);
+
+/*
+ * The same where every sequence continues one common prefix, held once: prefix_len positions behind
+ * the page list prefix_table_dev (ceil(prefix_len / page) entries). Row i meets all of the prefix
+ * and then its own sequence as in gptq_cache_attend (lengths count the own positions only; they may
+ * be 0). The prefix is met by the rows of all sequences together, so its codes are read and
+ * unpacked once per 128 or so rows instead of once per sequence.
+ *   prefix_len      0 .. 2^30, on the host.
+ *   ws_dev          gptq_cache_workspace_size(cache, n, ratio, 1) bytes.
+ * Other arguments, arithmetic and errors as gptq_cache_attend.
+ */
+gptq_status gptq_cache_attend_shared(const gptq_cache* cache, const gptq_cache_rows* rows,
+                                     const int32_t* prefix_table_dev, int64_t prefix_len,
+                                     const void* Q_dev, int64_t ldq, int ratio, float scale,
+                                     void* out_dev, int64_t ldo, void* ws_dev, size_t ws_bytes,
+                                     int32_t* info_dev, void* stream);
+
+/* Workspace bytes of gptq_cache_attend (shared = 0) or gptq_cache_attend_shared (1) for n rows on
+ * the current device; 0 for bad input. */
+size_t gptq_cache_workspace_size(const gptq_cache* cache, int64_t n, int ratio, int shared);
 
 /* Workspace bytes needed by one call (GPTQ_WS_PREPARE or GPTQ_WS_QUANTIZE); 0 for bad input. */
 size_t gptq_workspace_size(int which, int64_t rows, int64_t cols, int block);

@@ -12,3 +12,6 @@ from .rotation import (  # noqa: F401
     hadamard_block, rotation_matrix, rotate, rotate_abs_terms, weight_incoherence,
 )
 from .obq import obq_row, obq_quantize  # noqa: F401
+from .cache import (  # noqa: F401
+    bf16_up, grid_quantize, pack_rows, values as cache_values, attend, attend_bound,
+)

@@ -1,0 +1,126 @@
+"""Plain fp64 CPU oracle for the quantized key/value cache and the attention over it.
+
+TEST INFRASTRUCTURE ONLY, like gptq_oracle: only the tests may import it. It shares no code with
+the CUDA library.
+
+Sources (web pages, cited by title and section):
+  [BLOG]  "GPTQ second-order quantization" blog: "Group-wise quantization" (one scale and zero point
+          per group of values).
+
+Readings taken (the pages have no cache):
+  * The grid of a group is the layer quantizer's asymmetric min/max grid with its step rounded up to
+    bfloat16: lo = min(0, min x), hi = max(0, max x), step = (hi - lo) / (2^bits - 1) (0: lo = -1,
+    hi = 1), s = step rounded up to bf16, z = clamp(rint(-lo / s)), q = clamp(rint(x / s) + z), each
+    step rounded once in float32. A value that is not finite, or a step that is not, gives the group
+    a NaN scale and zero codes.
+  * Codes of a row are packed like the weights': code d in bits bits * (d mod (32 / bits)) of word
+    d // (32 / bits).
+  * Attention of one query over tokens t: sum_t w_t v_t / sum_t w_t with w_t = exp(scale q . k_t),
+    taken in fp64; no tokens give 0.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+
+def bf16_up(x: np.ndarray) -> np.ndarray:
+    """Positive float32 numbers rounded up to bfloat16 (as float32)."""
+    bits = np.ascontiguousarray(x, np.float32).view(np.uint32).astype(np.uint64)
+    return (((bits + 0xFFFF) >> 16) << 16).astype(np.uint32).view(np.float32)
+
+
+def grid_quantize(x: np.ndarray, bits: int, group: int):
+    """float32 x [..., dim] -> (codes uint8 [..., dim], scales float32 [..., dim / group] holding
+    bf16 values, zeros uint8 [..., dim / group])."""
+    x = np.asarray(x, np.float32)
+    v = x.reshape(*x.shape[:-1], -1, group)
+    top = np.float32(2 ** bits - 1)
+    with np.errstate(all="ignore"):
+        good = np.isfinite(v).all(-1)
+        safe = np.where(good[..., None], v, np.float32(0))
+        lo = np.minimum(safe.min(-1), np.float32(0))
+        hi = np.maximum(safe.max(-1), np.float32(0))
+        step = (hi - lo) / top
+        flat = step == 0
+        lo = np.where(flat, np.float32(-1), lo)
+        step = np.where(flat, np.float32(2) / top, step)
+        s = bf16_up(step)
+        good &= np.isfinite(s)
+        s = np.where(good, s, np.float32(1))
+        z = np.clip(np.rint(-lo / s), 0, top)
+        q = np.clip(np.rint(safe / s[..., None]) + z[..., None], 0, top)
+    s = np.where(good, s, np.float32(np.nan))
+    z = np.where(good, z, 0)
+    q = np.where(good[..., None], q, 0)
+    return q.reshape(x.shape).astype(np.uint8), s, z.astype(np.uint8)
+
+
+def pack_rows(codes: np.ndarray, bits: int) -> np.ndarray:
+    """uint8 codes [..., dim] -> uint32 words [..., dim * bits / 32]."""
+    per = 32 // bits
+    c = np.asarray(codes, np.uint32).reshape(*codes.shape[:-1], -1, per)
+    words = np.zeros(c.shape[:-1], np.uint32)
+    for i in range(per):
+        words |= c[..., i] << np.uint32(bits * i)
+    return words
+
+
+def values(codes: np.ndarray, scales: np.ndarray, zeros: np.ndarray) -> np.ndarray:
+    """s (q - z) in fp64."""
+    group = codes.shape[-1] // scales.shape[-1]
+    q = codes.astype(np.float64).reshape(*scales.shape, group)
+    v = scales.astype(np.float64)[..., None] * (q - zeros.astype(np.float64)[..., None])
+    return v.reshape(codes.shape)
+
+
+def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float) -> np.ndarray:
+    """One query [dim] over keys and values [tokens, dim], fp64."""
+    if k.shape[0] == 0:
+        return np.zeros(v.shape[-1])
+    x = (k @ q.astype(np.float64)) * scale
+    w = np.exp(x - x.max())
+    return (w @ v) / w.sum()
+
+
+def attend_bound(q, kc, ks, kz, vc, vs, vz, scale: float, image16: bool = False):
+    """One query [dim] over cached tokens: (the result, a bound on the error of a bf16 result of it),
+    per dimension, for a kernel with fp32 sums and fp16 operands. The arithmetic written out, nothing
+    measured. kc, vc: codes [tokens, dim]; ks, kz, vs, vz: their grids [tokens, groups].
+
+    * The sums q . code take dim / 16 + 8 steps, each off by 2^-22 of the magnitudes it adds: x_t
+      moves by (dim / 16 + 8) 2^-22 A_t, A_t = scale sum_groups s (sum |q| code + z sum |q|). The
+      exponential, the logarithm and the products around them add 2^-20. With `image16` the keys are
+      fp16 images of s (code - z), off by 2^-12 each: x_t moves by 2^-12 scale sum |q k| more. A
+      relative error e of the weights moves the result by at most 2 e sum p |v|.
+    * Each weight is rounded to fp16: by 2^-12 of itself, or by 2^-25 of the unit in which the
+      largest is at least 1. With `image16` each value is too, by 2^-12 of itself or 2^-36 of the
+      largest.
+    * The sum over tokens runs in steps of 16 and is joined from parts: (tokens / 16 + 64) 2^-22 of
+      sum p |v|.
+    * The result is rounded to bf16: half a step, 2^-8 of the value that is rounded.
+    """
+    T, dim = kc.shape
+    if T == 0:
+        return np.zeros(dim), np.zeros(dim)
+    G = ks.shape[1]
+    q = q.astype(np.float64)
+    k, v = values(kc, ks, kz), values(vc, vs, vz)
+    x = (k @ q) * scale
+    p = np.exp(x - x.max())
+    p /= p.sum()
+    out, mass = p @ v, p @ np.abs(v)
+    aq = np.abs(q).reshape(G, -1)
+    A = scale * (ks.astype(np.float64) *
+                 (np.einsum("tgd,gd->tg", kc.astype(np.float64).reshape(T, G, -1), aq) +
+                  kz * aq.sum(-1))).sum(1)
+    e = (dim / 16 + 8) * 2.0 ** -22 * A.max() + 2.0 ** -20
+    steps = (T / 16 + 64) * 2.0 ** -22
+    if image16:
+        e += 2.0 ** -12 * scale * (np.abs(k) @ np.abs(q)).max()
+        bound = mass * (2 * e + 2.0 ** -11 + steps) + \
+            2.0 ** -25 * p.max() * np.abs(v).sum(0) + 2.0 ** -36 * np.abs(v).max()
+    else:
+        unit = (p[:, None] * vs.astype(np.float64)).max()
+        z = np.repeat(vz.astype(np.float64), dim // G, 1)
+        bound = mass * (2 * e + 2.0 ** -12 + steps) + 2.0 ** -25 * unit * np.abs(vc - z).sum(0)
+    return out, bound + 2.0 ** -8 * (np.abs(out) + bound)

@@ -18,6 +18,7 @@ GPTQ_BF16, GPTQ_FP32 = 0, 1
 GPTQ_INFO_TIMEOUT = -1
 GPTQ_INFO_BAD_HESSIAN = -2
 GPTQ_INFO_BAD_CODE = -3
+GPTQ_INFO_BAD_PAGE = -4
 GPTQ_WS_PREPARE, GPTQ_WS_QUANTIZE = 1, 2
 GPTQ_ROUTE_DEFAULT, GPTQ_ROUTE_THREE_STEP, GPTQ_ROUTE_REVERSED = 0, 1, 2
 GPTQ_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
@@ -25,6 +26,21 @@ GPTQ_OBQ_NATURAL, GPTQ_OBQ_GREEDY = 0, 1
 
 # name -> (restype, argtypes)
 _P, _I64, _I32, _F, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+
+
+class Cache(ctypes.Structure):
+    """gptq_cache: the tensors and shape of a quantized key/value cache."""
+    _fields_ = [(h + "_" + part, _P) for h in "kv" for part in ("codes", "scales", "zeros")] + \
+        [("pages", _I64)] + [(k, _I32) for k in ("heads", "page", "dim", "bits", "group")]
+
+
+class CacheRows(ctypes.Structure):
+    """gptq_cache_rows: the rows of a cache call and where they sit."""
+    _fields_ = [("table", _P), ("ld_table", _I64), ("width", _I32), ("lengths", _P),
+                ("starts", _P), ("batch", _I64), ("n", _I64)]
+
+
+_PC, _PR = ctypes.POINTER(Cache), ctypes.POINTER(CacheRows)
 SIGNATURES = {
     "gptq_hessian_accumulate": (_I32, [_P, _I64, _P, _I32, _I64, _I64, _P, _P]),
     "gptq_prepare_hinv": (_I32, [_P, _P, _I64, _I64, _F, _P, _SZ, _P, _P]),
@@ -46,6 +62,12 @@ SIGNATURES = {
     "gptq_hadamard_rotate": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _P, _I32, _I64, _P]),
     "gptq_w4a16_matmul": (_I32, [_P, _P, _P, _I64, _I64, _I32, _P, _I32, _I64, _I64, _P, _I64, _P,
                                  _P]),
+    "gptq_cache_append": (_I32, [_PC, _PR, _P, _I64, _P, _I64, _I32, _P, _P, _P, _P]),
+    "gptq_cache_read": (_I32, [_PC, _PR, _P, _P, _I32, _P, _P]),
+    "gptq_cache_attend": (_I32, [_PC, _PR, _P, _I64, _I32, _F, _P, _I64, _P, _SZ, _P, _P]),
+    "gptq_cache_attend_shared": (_I32, [_PC, _PR, _P, _I64, _P, _I64, _I32, _F, _P, _I64, _P, _SZ,
+                                        _P, _P]),
+    "gptq_cache_workspace_size": (_SZ, [_PC, _I64, _I32, _I32]),
     "gptq_selftest_gemm": (_I32, [_P, _I64, _I32, _P, _I64, _I32, _P, _I64, _I32, _I32, _I32,
                                   _F, _F, _I32, _I32, _I32, _P, _P, _P, _SZ, _P, _P]),
     "gptq_selftest_wait_timeout": (_I32, [_P, _I32, _P]),
@@ -249,6 +271,89 @@ def obq_quantize(W, Hinv, bits, codes, W_hat, order=None, loss=None, scales=None
         GPTQ_OBQ_GREEDY if greedy else GPTQ_OBQ_NATURAL, _ptr(codes), _ptr(W_hat), _ptr(order),
         _ptr(loss), _ptr(scales), _ptr(zeros), _stream(stream))
     _check(st, "gptq_obq_quantize")
+
+
+def cache_rows(n, table, lengths, starts):
+    """CacheRows of n rows: int32 tensors table [batch, width], lengths [batch] and starts
+    [batch + 1] or None (row b is the last position of sequence b)."""
+    import torch
+    for name, t in (("table", table), ("lengths", lengths), ("starts", starts)):
+        if t is not None and t.dtype != torch.int32:
+            raise TypeError(f"{name} must be int32")
+    ld = _row_major_ld(table, "table") if table.shape[1] > 1 else max(1, table.stride(0))
+    batch = table.shape[0]
+    for name, t, size in (("lengths", lengths, batch), ("starts", starts, batch + 1)):
+        if t is not None and (t.shape != (size,) or (size > 1 and t.stride(0) != 1)):
+            raise ValueError(f"{name} must be a dense vector of {size}")
+    return CacheRows(_ptr(table), max(ld, table.shape[1]), table.shape[1], _ptr(lengths),
+                     _ptr(starts), batch, int(n))
+
+
+def _heads_ld(t, name, heads, dim):
+    """Row stride of a [n, heads, dim] tensor whose rows are dense."""
+    if t.dim() != 3 or t.shape[1:] != (heads, dim):
+        raise ValueError(f"{name} must be [n, {heads}, {dim}]")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name} must hold the heads of a row one after another")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * dim)
+
+
+def _same_rows(t, like, name):
+    if t is not None and (t.shape != like.shape or t.dtype != like.dtype or
+                          not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(like.shape)} and "
+                         f"type {like.dtype}")
+
+
+def cache_append(cache, rows, K, V, K_hat=None, V_hat=None, info=None, stream=None):
+    """Quantizes K, V [n, heads, dim] (bf16 or fp32) into their positions (gptq_cache_append)."""
+    ldk = _heads_ld(K, "K", cache.heads, cache.dim)
+    ldv = _heads_ld(V, "V", cache.heads, cache.dim)
+    if V.shape != K.shape or V.dtype != K.dtype:
+        raise ValueError("K and V must have the same shape and type")
+    _same_rows(K_hat, K, "K_hat")
+    _same_rows(V_hat, V, "V_hat")
+    st = load().gptq_cache_append(cache, rows, _ptr(K), ldk, _ptr(V), ldv, _dtype_code(K),
+                                  _ptr(K_hat), _ptr(V_hat), _ptr(info), _stream(stream))
+    _check(st, "gptq_cache_append")
+
+
+def cache_read(cache, rows, K_out, V_out, info=None, stream=None):
+    """Reads positions back into contiguous K_out, V_out [n, heads, dim] (bf16 or fp32; one of
+    them may be None) (gptq_cache_read)."""
+    like = K_out if K_out is not None else V_out
+    if like is None:
+        raise ValueError("K_out and V_out are both None")
+    _heads_ld(like, "output", cache.heads, cache.dim)
+    _same_rows(K_out, like, "K_out")
+    _same_rows(V_out, like, "V_out")
+    st = load().gptq_cache_read(cache, rows, _ptr(K_out), _ptr(V_out), _dtype_code(like),
+                                _ptr(info), _stream(stream))
+    _check(st, "gptq_cache_read")
+
+
+def cache_workspace_size(cache, n, ratio, shared) -> int:
+    return int(load().gptq_cache_workspace_size(cache, int(n), int(ratio), int(shared)))
+
+
+def cache_attend(cache, rows, Q, out, ratio, scale, ws, info=None, stream=None, prefix_table=None,
+                 prefix_len=None):
+    """Attention of Q [n, heads * ratio, dim] (bf16) into out; with prefix_len, over a common
+    prefix too (gptq_cache_attend, gptq_cache_attend_shared)."""
+    import torch
+    ldq = _heads_ld(Q, "Q", cache.heads * ratio, cache.dim)
+    ldo = _heads_ld(out, "out", cache.heads * ratio, cache.dim)
+    if Q.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
+        raise TypeError("Q and out must be bfloat16")
+    if out.shape != Q.shape:
+        raise ValueError("Q and out must have the same shape")
+    tail = (_ptr(Q), ldq, int(ratio), float(scale), _ptr(out), ldo, _ptr(ws),
+            ws.numel() * ws.element_size(), _ptr(info), _stream(stream))
+    if prefix_len is None:
+        _check(load().gptq_cache_attend(cache, rows, *tail), "gptq_cache_attend")
+    else:
+        _check(load().gptq_cache_attend_shared(cache, rows, _ptr(prefix_table), int(prefix_len),
+                                               *tail), "gptq_cache_attend_shared")
 
 
 def selftest_gemm(A, a_mn, B, b_mn, C, M, N, K, alpha=1.0, beta=0.0, lower=False,

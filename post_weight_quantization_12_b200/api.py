@@ -16,9 +16,17 @@ rotated before quantization:
     lin = pack_4bit(out)                      # PackedLinear4: packed codes, scales, zeros
     Y = lin(X)                                # fp32 [n, rows] = X W_hat^T for bf16 X [n, cols]
     Wr, Xr = rotate(W, signs), rotate(X, signs)   # data-free randomized Hadamard rotation
+
+The keys and values of the layers' attention go into a quantized cache, and a decode step attends
+to it without unpacking it in memory:
+
+    cache = QuantizedCache(pages, heads, dim, page=64, bits=4)
+    cache.append(K, V, table, lengths)        # one new token per sequence (or starts= for more)
+    O = cache.attend(Q, table, lengths)       # bf16 [n, q_heads, dim]
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 
 import torch
@@ -205,3 +213,132 @@ def rotate(X: torch.Tensor, sign_bits=None, out=None, stream=None) -> torch.Tens
     _lib.hadamard_rotate(X, out, sign_bits, stream)
     return out
 
+
+
+class QuantizedCache:
+    """Paged key/value cache on 4- or 8-bit grids: one grid per (token, head, `group` dimensions).
+
+    Every call takes the same description of its n rows: `table` int32 [batch, width] (page of
+    positions page * k .. page * k + page - 1 of sequence b at [b, k]), `lengths` int32 [batch] and
+    `starts` int32 [batch + 1] or None. Rows starts[b] .. starts[b + 1] - 1 are the last positions
+    of sequence b, the very last one at lengths[b] - 1; without starts, row b is the last position
+    of sequence b. A step appends with the lengths after it and attends with the same ones. The
+    index tensors are read on the device, so a captured step can be replayed with new values in
+    them; rows behind starts[batch] are ignored.
+
+    Calls run on `stream` (default: the current stream of the cache's device) and allocate their
+    workspace there. `info` is the device status word: nonzero once a call met a position without
+    a page (see _lib.GPTQ_INFO_BAD_PAGE)."""
+
+    def __init__(self, pages: int, heads: int, dim: int, page: int = 64, bits: int = 4,
+                 group: int = -1, device="cuda"):
+        group = dim if group == -1 else group
+        if group <= 0 or dim % group:
+            raise ValueError("group must divide dim")
+        if bits not in (4, 8):
+            raise ValueError("bits must be 4 or 8")
+        words, groups = (pages, heads, page, dim * bits // 32), (pages, heads, page, dim // group)
+        t = [torch.zeros(shape, dtype=dt, device=device) for _ in range(2)
+             for shape, dt in ((words, torch.int32), (groups, torch.bfloat16),
+                               (groups, torch.uint8))]
+        self._adopt(t, dim)
+
+    @classmethod
+    def of_tensors(cls, k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros, dim: int):
+        """A cache over existing tensors: codes int32 [pages, heads, page, dim * bits / 32], scales
+        bf16 and zeros uint8 [pages, heads, page, dim / group]."""
+        self = cls.__new__(cls)
+        self._adopt([k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros], int(dim))
+        return self
+
+    def _adopt(self, tensors, dim):
+        codes, scales = tensors[0], tensors[1]
+        if codes.dim() != 4 or scales.dim() != 4:
+            raise ValueError("codes and scales must be [pages, heads, page, ...]")
+        pages, heads, page, words = codes.shape
+        groups = scales.shape[3]
+        if dim <= 0 or 32 * words % dim or groups <= 0 or dim % groups:
+            raise ValueError(f"{words} words and {groups} grids a row do not fit dim {dim}")
+        for i, t in enumerate(tensors):
+            name = "kv"[i // 3] + "_" + ("codes", "scales", "zeros")[i % 3]
+            want = (torch.int32, torch.bfloat16, torch.uint8)[i % 3]
+            if t.dtype != want or t.shape != (pages, heads, page, words if i % 3 == 0 else groups):
+                raise ValueError(f"{name} must be {want} [{pages}, {heads}, {page}, "
+                                 f"{words if i % 3 == 0 else groups}]")
+            if not t.is_contiguous() or t.device != codes.device:
+                raise ValueError(f"{name} must be contiguous and on the device of k_codes")
+            setattr(self, name, t)
+        self.pages, self.heads, self.page, self.dim = pages, heads, page, dim
+        self.bits, self.group = 32 * words // dim, dim // groups
+        self.device = codes.device
+        self.info = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._c = _lib.Cache(*(t.data_ptr() for t in tensors), pages, heads, page, dim, self.bits,
+                             self.group)
+
+    @contextlib.contextmanager
+    def _on(self, stream, *tensors):
+        """The cache's device and the stream of the call, current for what the call allocates."""
+        for t in tensors:
+            if t is not None and t.device != self.device:
+                raise ValueError(f"a tensor is on {t.device}, the cache on {self.device}")
+        with torch.cuda.device(self.device):
+            if stream is None:
+                yield torch.cuda.current_stream()
+                return
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), self.device)
+            with torch.cuda.stream(stream):
+                yield stream
+
+    def append(self, K, V, table, lengths, starts=None, K_hat=None, V_hat=None, stream=None):
+        """Quantizes the rows K, V [n, heads, dim] (bf16 or fp32) into their positions. K_hat and
+        V_hat, if given, receive what the cache now holds of them, s (q - z)."""
+        with self._on(stream, K, V, table, lengths, starts, K_hat, V_hat) as s:
+            _lib.cache_append(self._c, _lib.cache_rows(K.shape[0], table, lengths, starts), K, V,
+                              K_hat, V_hat, self.info, s)
+
+    def read(self, table, lengths, starts=None, n=None, dtype=torch.bfloat16, K_out=None,
+             V_out=None, stream=None):
+        """The values of the rows' positions, (K, V) [n, heads, dim]; n as the outputs given, or
+        as asked for (default: one row per sequence)."""
+        with self._on(stream, table, lengths, starts, K_out, V_out) as s:
+            like = K_out if K_out is not None else V_out
+            if like is None:
+                n = table.shape[0] if n is None else int(n)
+                K_out = torch.empty(n, self.heads, self.dim, dtype=dtype, device=self.device)
+                V_out = torch.empty_like(K_out)
+                like = K_out
+            _lib.cache_read(self._c, _lib.cache_rows(like.shape[0], table, lengths, starts),
+                            K_out, V_out, self.info, s)
+            return K_out, V_out
+
+    def _attend(self, Q, table, lengths, starts, scale, out, stream, prefix_table, prefix_len):
+        with self._on(stream, Q, table, lengths, starts, out, prefix_table) as s:
+            if Q.dim() != 3 or Q.shape[1] % self.heads or not Q.shape[1]:
+                raise ValueError(f"Q must be [n, k * {self.heads}, {self.dim}]")
+            ratio = Q.shape[1] // self.heads
+            if out is None:
+                out = torch.empty(Q.shape, dtype=Q.dtype, device=self.device)
+            size = _lib.cache_workspace_size(self._c, Q.shape[0], ratio, prefix_len is not None)
+            ws = torch.empty(size, dtype=torch.uint8, device=self.device)
+            _lib.cache_attend(self._c, _lib.cache_rows(Q.shape[0], table, lengths, starts), Q, out,
+                              ratio, self.dim ** -0.5 if scale is None else scale, ws, self.info,
+                              s, prefix_table, prefix_len)
+            return out
+
+    def attend(self, Q, table, lengths, starts=None, scale=None, out=None, stream=None):
+        """Causal softmax attention of Q [n, q_heads, dim] (bf16; q_heads a multiple of heads) over
+        the rows' sequences, up to each row's position; scale defaults to dim ** -0.5."""
+        return self._attend(Q, table, lengths, starts, scale, out, stream, None, None)
+
+    def attend_shared(self, Q, prefix_table, prefix_len, table, lengths, starts=None, scale=None,
+                      out=None, stream=None):
+        """The same where every sequence continues one common prefix of `prefix_len` positions
+        behind the pages `prefix_table` int32 [k]: its pages are met once for all rows. `lengths`
+        count the own positions only."""
+        prefix_len = int(prefix_len)
+        if prefix_len < 0 or prefix_table.dim() != 1 or prefix_table.dtype != torch.int32 or \
+                not prefix_table.is_contiguous() or \
+                prefix_table.shape[0] * self.page < prefix_len:
+            raise ValueError("prefix_table must be a dense int32 vector that covers prefix_len")
+        return self._attend(Q, table, lengths, starts, scale, out, stream, prefix_table, prefix_len)

@@ -7,6 +7,7 @@
 #include <mutex>
 #include <utility>
 
+#include "cache.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -268,6 +269,149 @@ gptq_status gptq_obq_quantize(const float* W_dev, int64_t rows, int64_t cols, in
   return run_obq_quantize(W_dev, rows, cols, ldw, Hinv_dev, bits, order_mode == GPTQ_OBQ_GREEDY,
                           codes_dev, W_hat_dev, order_dev, loss_dev, scales_dev, zeros_dev,
                           static_cast<cudaStream_t>(stream));
+}
+
+static bool power_of_two(int v) { return v > 0 && (v & (v - 1)) == 0; }
+
+// The checks of a cache and its rows, and their form for the kernels.
+static gptq_status check_cache(const gptq_cache* c, CacheView* view) {
+  if (c == nullptr || c->pages <= 0 || c->heads <= 0 || c->page <= 0 || c->dim <= 0 ||
+      c->group <= 0 || c->dim % c->group != 0)
+    return GPTQ_EINVAL;
+  if ((c->dim != 64 && c->dim != 128) || (c->bits != 4 && c->bits != 8) ||
+      (c->group != 32 && c->group != 64 && c->group != 128) || !power_of_two(c->page) ||
+      c->page < 16 || c->page > 32768)
+    return GPTQ_EUNSUPPORTED;
+  if (c->heads > (1 << 16) || c->pages > INT32_MAX ||
+      c->pages > (static_cast<int64_t>(1) << 40) / c->heads / c->page / c->dim)
+    return GPTQ_EUNSUPPORTED;
+  if (view == nullptr) return GPTQ_OK;
+  const void* p[6] = {c->k_codes_dev, c->k_scales_dev, c->k_zeros_dev,
+                      c->v_codes_dev, c->v_scales_dev, c->v_zeros_dev};
+  for (int i = 0; i < 6; ++i) {
+    if (p[i] == nullptr || !aligned(p[i], 16)) return GPTQ_EINVAL;
+    for (int j = 0; j < i; ++j)
+      if (p[i] == p[j]) return GPTQ_EINVAL;
+  }
+  view->half[0] = {reinterpret_cast<uint8_t*>(c->k_codes_dev), c->k_scales_dev, c->k_zeros_dev};
+  view->half[1] = {reinterpret_cast<uint8_t*>(c->v_codes_dev), c->v_scales_dev, c->v_zeros_dev};
+  view->pages = c->pages;
+  view->heads = c->heads;
+  view->page_shift = 0;
+  while ((1 << view->page_shift) < c->page) ++view->page_shift;
+  return GPTQ_OK;
+}
+
+static gptq_status check_rows(const gptq_cache_rows* r, int64_t values_per_row, CacheView* view,
+                              CacheRows* rows) {
+  if (r == nullptr || r->n < 0 || r->batch < 0 || r->width < 0 || r->ld_table < r->width)
+    return GPTQ_EINVAL;
+  if (r->n > INT32_MAX || r->batch > INT32_MAX || r->ld_table > INT32_MAX ||
+      r->n > (static_cast<int64_t>(1) << 40) / values_per_row)
+    return GPTQ_EUNSUPPORTED;
+  if (r->starts_dev == nullptr && r->n > r->batch) return GPTQ_EINVAL;
+  if (r->n > 0 && r->batch > 0 &&
+      (r->lengths_dev == nullptr || (r->width > 0 && r->table_dev == nullptr)))
+    return GPTQ_EINVAL;
+  if (!aligned(r->table_dev, 4) || !aligned(r->lengths_dev, 4) || !aligned(r->starts_dev, 4))
+    return GPTQ_EINVAL;
+  view->width = r->width;
+  *rows = {r->table_dev, r->ld_table, r->lengths_dev, r->starts_dev,
+           r->starts_dev == nullptr ? r->n : r->batch, r->n};
+  return GPTQ_OK;
+}
+
+gptq_status gptq_cache_append(const gptq_cache* cache, const gptq_cache_rows* rows,
+                              const void* K_dev, int64_t ldk, const void* V_dev, int64_t ldv,
+                              gptq_dtype dtype, void* K_hat_dev, void* V_hat_dev,
+                              int32_t* info_dev, void* stream) {
+  CacheView c;
+  CacheRows r;
+  gptq_status st = check_cache(cache, &c);
+  if (st != GPTQ_OK) return st;
+  const int64_t width = static_cast<int64_t>(cache->heads) * cache->dim;
+  if ((st = check_rows(rows, width, &c, &r)) != GPTQ_OK) return st;
+  if (dtype != GPTQ_BF16 && dtype != GPTQ_FP32) return GPTQ_EINVAL;
+  const int64_t e = dtype == GPTQ_BF16 ? 2 : 4;
+  if (ldk < width || ldv < width || (ldk * e) % 16 != 0 || (ldv * e) % 16 != 0) return GPTQ_EINVAL;
+  if (r.n == 0 || r.batch == 0) return GPTQ_OK;  // no rows: the buffers may be absent
+  if (K_dev == nullptr || V_dev == nullptr || !aligned(K_dev, 16) || !aligned(V_dev, 16) ||
+      !aligned(K_hat_dev, 16) || !aligned(V_hat_dev, 16))
+    return GPTQ_EINVAL;
+  return run_cache_append(c, r, cache->dim, cache->bits, cache->group, K_dev, ldk, V_dev, ldv,
+                          dtype == GPTQ_BF16, K_hat_dev, V_hat_dev, info_dev,
+                          static_cast<cudaStream_t>(stream));
+}
+
+gptq_status gptq_cache_read(const gptq_cache* cache, const gptq_cache_rows* rows, void* K_out_dev,
+                            void* V_out_dev, gptq_dtype dtype, int32_t* info_dev, void* stream) {
+  CacheView c;
+  CacheRows r;
+  gptq_status st = check_cache(cache, &c);
+  if (st != GPTQ_OK) return st;
+  if ((st = check_rows(rows, static_cast<int64_t>(cache->heads) * cache->dim, &c, &r)) != GPTQ_OK)
+    return st;
+  if (dtype != GPTQ_BF16 && dtype != GPTQ_FP32) return GPTQ_EINVAL;
+  if (r.n == 0 || r.batch == 0) return GPTQ_OK;
+  if ((K_out_dev == nullptr && V_out_dev == nullptr) || !aligned(K_out_dev, 16) ||
+      !aligned(V_out_dev, 16))
+    return GPTQ_EINVAL;
+  return run_cache_read(c, r, cache->dim, cache->bits, cache->group, K_out_dev, V_out_dev,
+                        dtype == GPTQ_BF16, info_dev, static_cast<cudaStream_t>(stream));
+}
+
+static gptq_status attend_checked(const gptq_cache* cache, const gptq_cache_rows* rows,
+                                  const int32_t* prefix_table_dev, int64_t prefix_len, bool shared,
+                                  const void* Q_dev, int64_t ldq, int ratio, float scale,
+                                  void* out_dev, int64_t ldo, void* ws_dev, size_t ws_bytes,
+                                  int32_t* info_dev, void* stream) {
+  CacheView c;
+  CacheRows r;
+  gptq_status st = check_cache(cache, &c);
+  if (st != GPTQ_OK) return st;
+  if (ratio < 1 || ratio > 1024) return GPTQ_EINVAL;
+  const int64_t width = static_cast<int64_t>(cache->heads) * ratio * cache->dim;
+  if ((st = check_rows(rows, width, &c, &r)) != GPTQ_OK) return st;
+  if (ldq < width || ldo < width || ldq % 8 != 0 || ldo % 8 != 0) return GPTQ_EINVAL;
+  if (!(scale >= -1e30f && scale <= 1e30f)) return GPTQ_EINVAL;
+  if (prefix_len < 0) return GPTQ_EINVAL;
+  if (prefix_len > (static_cast<int64_t>(1) << 30)) return GPTQ_EUNSUPPORTED;
+  if (r.n == 0 || r.batch == 0) return GPTQ_OK;
+  if (Q_dev == nullptr || out_dev == nullptr || Q_dev == out_dev || !aligned(Q_dev, 16) ||
+      !aligned(out_dev, 16))
+    return GPTQ_EINVAL;
+  if (prefix_len > 0 && (prefix_table_dev == nullptr || !aligned(prefix_table_dev, 4)))
+    return GPTQ_EINVAL;
+  if (ws_dev == nullptr || !aligned(ws_dev, 256) ||
+      ws_bytes < cache_workspace_bytes(cache->heads, cache->dim, r.n, ratio, shared))
+    return GPTQ_EWORKSPACE;
+  CacheQuery q{static_cast<const __nv_bfloat16*>(Q_dev), ldq, ratio, scale,
+               static_cast<__nv_bfloat16*>(out_dev), ldo, prefix_table_dev, prefix_len};
+  return run_cache_attend(c, r, cache->dim, cache->bits, cache->group, q, ws_dev, info_dev,
+                          static_cast<cudaStream_t>(stream));
+}
+
+gptq_status gptq_cache_attend(const gptq_cache* cache, const gptq_cache_rows* rows,
+                              const void* Q_dev, int64_t ldq, int ratio, float scale, void* out_dev,
+                              int64_t ldo, void* ws_dev, size_t ws_bytes, int32_t* info_dev,
+                              void* stream) {
+  return attend_checked(cache, rows, nullptr, 0, false, Q_dev, ldq, ratio, scale, out_dev, ldo,
+                        ws_dev, ws_bytes, info_dev, stream);
+}
+
+gptq_status gptq_cache_attend_shared(const gptq_cache* cache, const gptq_cache_rows* rows,
+                                     const int32_t* prefix_table_dev, int64_t prefix_len,
+                                     const void* Q_dev, int64_t ldq, int ratio, float scale,
+                                     void* out_dev, int64_t ldo, void* ws_dev, size_t ws_bytes,
+                                     int32_t* info_dev, void* stream) {
+  return attend_checked(cache, rows, prefix_table_dev, prefix_len, true, Q_dev, ldq, ratio, scale,
+                        out_dev, ldo, ws_dev, ws_bytes, info_dev, stream);
+}
+
+size_t gptq_cache_workspace_size(const gptq_cache* cache, int64_t n, int ratio, int shared) {
+  if (check_cache(cache, nullptr) != GPTQ_OK || n < 0 || n > INT32_MAX || ratio < 1 || ratio > 1024)
+    return 0;
+  return cache_workspace_bytes(cache->heads, cache->dim, n, ratio, shared != 0);
 }
 
 size_t gptq_workspace_size(int which, int64_t rows, int64_t cols, int block) {

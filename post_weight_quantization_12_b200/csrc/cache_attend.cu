@@ -1,0 +1,974 @@
+// Attention of a few rows per sequence over the quantized key/value cache.
+//
+// A row is one query token and head. With x_t = c log2(e) (q . k_t) over the positions t that the
+// row meets, k_t and v_t read as s (code - z) per group of head dimensions,
+//   o = sum_t 2^(x_t) v_t / sum_t 2^(x_t),
+// taken in one pass over the cache. The rows of one cache head (its query heads, and the sequence's
+// tokens) form the 8 or 16 columns of tensor-core products whose other operand is the codes:
+//   x:  codes of 16 tokens (the product's rows) against the queries,
+//   o:  codes of 16 head dimensions against the weights of 16 tokens.
+// The codes enter as fp16 numbers without any conversion: an integer below 1024 in the low bits of
+// an fp16 word is that integer times 2^-24 exactly (a subnormal), so a mask (and for the odd codes
+// a byte permute) makes the operand. Zero points and scales are applied outside the products:
+//   q . k_t = s_t ((q . code_t) - z_t sum(q))             scale and zero of token t, per group
+// For o the zero points are subtracted from the operand itself (exact in fp16): a running sum of
+// codes, all positive, would lose 2^-24 of itself with each product, the tensor core's sums being
+// cut towards zero, and what is left after the zero points' share is a small part of it.
+// The queries are fp16 after a power-of-two scale per row (bf16's 8 bits fit in fp16's 11; values
+// 2^-38 below the row's largest are lost). The weights w_t s_t become fp16 (rounding 2^-12 of each)
+// relative to their own running maximum: with u_t = x_t + log2(s_t) and M >= max u - 8 the operand
+// is 2^(u_t - M), whatever range the scales have, and the denominator sums 2^(u_t - M) / s_t. Sums,
+// maxima and denominators are fp32.
+//
+// The work is cut evenly: tiles of 64 tokens of all (sequence, head, row tile) items are numbered
+// in order and each CTA takes one run of them. A run that covers an item writes its output; an item
+// that several runs share is joined from their partial results by a second kernel.
+// What bounds it: HBM for long sequences (bits / 8 + 3 / group bytes a value); every warp keeps
+// three steps of 16 tokens (2 to 4 KB each) in flight through its own ring of cp.async copies, each
+// lane fetching just the codes that it will consume.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "cache.cuh"
+
+namespace gptq {
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kStep = 16;                   // tokens of one warp step
+constexpr int kTile = kStep * kWarps;       // tokens of one tile of work
+constexpr int kStages = 4;                  // ring depth of a warp, in steps
+constexpr int kMaxResident = 4;             // CTAs per SM
+constexpr float kScaleFloor = 1.2621774e-29f;   // 2^-96, see below
+constexpr float kNegInf = -INFINITY;
+
+template <int D, int BITS, int GROUP, int NT>
+struct Cfg {
+  static constexpr int G = D / GROUP;
+  static constexpr int RB = D * BITS / 8;                     // bytes of a row of codes
+  static constexpr int NP = G > RB / 64 ? G : RB / 64;        // K pieces a lane takes of a row
+  static constexpr int NPS = NP < 1 ? 1 : NP;
+  static constexpr int CPB = RB / 4 / NPS;                    // bytes of a K piece: 4, 8 or 16
+  static constexpr int VGB = GROUP * BITS / 64;               // bytes of a lane's V share of a group
+  static constexpr int VB = VGB < 4 ? 4 : VGB;                // ... and what it fetches
+  static constexpr int kK = kStep * RB;                       // K bytes of a stage
+  static constexpr int kV = kStep * 8 * G * VB;               // V bytes of a stage
+  static constexpr int kGridBytes = 96 * G;                   // scales and zeros of 16 tokens
+  static constexpr int kStage = kK + kV + kGridBytes;
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int R = 8 * NT;                            // rows of a row tile
+  static constexpr int kPad = D + 4;
+  static constexpr int kJoin = kWarps * R * kPad * 4;         // fp32 results of the warps
+  static constexpr int kSmem = (kWarps * kRing > kJoin ? kWarps * kRing : kJoin);
+};
+
+// One level of attention: the rows meet the positions of their own sequence (causal), or all of
+// them the first `fixed_len` positions behind one page table.
+struct Level {
+  CacheView cache;
+  CacheRows rows;
+  int64_t fixed_len;            // < 0: lengths and starts of `rows`
+  const __nv_bfloat16* q;
+  int64_t ldq;
+  int ratio;
+  float scale_log2;             // c log2(e)
+  __nv_bfloat16* out;           // final output, or null: `mid` is written instead
+  int64_t ldo;
+  float* mid;                   // [n][heads ratio][D] fp32 results of the level before, and its lse
+  float* mid_lse;               // read if `out` is set and they are not null
+  float* part;                  // [2 grid][R][D], partial results
+  float* part_lse;              // [2 grid][R]
+  int32_t* join;                // [grid][8]: what the run's last item needs joined
+  int32_t* info;
+};
+
+struct Sequence {
+  int64_t row0, end;            // rows row0 .. row0 + count - 1; end: the nominal end
+  int64_t count, len, tiles;    // tiles of the whole sequence over all heads
+  int row_tiles;
+  int64_t tiles_per;            // of one (head, row tile)
+};
+
+template <int R>
+__device__ __forceinline__ Sequence get_sequence(const Level& a, int64_t b) {
+  Sequence s;
+  if (a.fixed_len >= 0) {
+    s.row0 = 0;
+    s.end = s.count = a.rows.n;
+    s.len = a.fixed_len;
+  } else {
+    s.row0 = b;
+    s.end = b + 1;
+    if (a.rows.starts != nullptr) {
+      s.row0 = max(__ldg(a.rows.starts + b), 0);
+      s.end = __ldg(a.rows.starts + b + 1);
+    }
+    s.count = max(min(s.end, a.rows.n) - s.row0, static_cast<int64_t>(0));
+    s.len = __ldg(a.rows.lengths + b);
+  }
+  const int64_t cap = static_cast<int64_t>(a.cache.width) << a.cache.page_shift;
+  if (s.len < 0 || s.len > cap) {
+    if (threadIdx.x == 0) record_info(a.info, GPTQ_INFO_BAD_PAGE);
+    s.len = s.len < 0 ? 0 : cap;
+  }
+  s.row_tiles = static_cast<int>((s.count * a.ratio + R - 1) / R);
+  s.tiles_per = max((s.len + kTile - 1) / kTile, static_cast<int64_t>(1));
+  s.tiles = s.tiles_per * s.row_tiles * a.cache.heads;
+  return s;
+}
+
+// The cut of the tiles of all sequences into runs, one per CTA and none of them empty; and for run
+// `part` the sequence that its first tile lies in, with the number of that sequence's first tile.
+struct Find {
+  int64_t warp_sum[kWarps];
+  int64_t b, base;
+};
+struct Cut {
+  int64_t total, parts;
+  __device__ __forceinline__ int64_t begin(int64_t part) const {
+    return total / parts * part + total % parts * part / parts;
+  }
+};
+template <int R>
+__device__ __forceinline__ Cut find_tile(const Level& a, int64_t part, Find& sh) {
+  const int64_t batch = a.fixed_len >= 0 ? 1 : a.rows.batch;
+  const int64_t per = (batch + kThreads - 1) / kThreads;
+  const int64_t b0 = min(threadIdx.x * per, batch), b1 = min(b0 + per, batch);
+  int64_t sum = 0;
+  for (int64_t b = b0; b < b1; ++b) sum += get_sequence<R>(a, b).tiles;
+  int64_t incl = sum;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sh.warp_sum[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += sh.warp_sum[w];
+    total += sh.warp_sum[w];
+  }
+  incl += before;
+  const Cut cut{total, max(min(total, static_cast<int64_t>(gridDim.x)), static_cast<int64_t>(1))};
+  const int64_t begin = part < cut.parts ? cut.begin(part) : total;
+  if (incl - sum <= begin && begin < incl) {
+    int64_t base = incl - sum;
+    int64_t b = b0;
+    for (; b + 1 < b1; ++b) {
+      const int64_t t = get_sequence<R>(a, b).tiles;
+      if (begin < base + t) break;
+      base += t;
+    }
+    sh.b = b;
+    sh.base = base;
+  }
+  __syncthreads();
+  return cut;
+}
+
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int bytes) {
+  if (bytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else if (bytes == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+// Byte permute with all four selector bits: 8 | i repeats the sign of byte i, here 0 or 255.
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 half2_floats(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+// Where the results of one row go: the final output (joined with the level before, if any), or the
+// fp32 results that the next level will join.
+template <int D>
+__device__ __forceinline__ void finish(const Level& a, int64_t tok, int qhead, int d, float4 o,
+                                       float lse) {
+  const int heads = a.cache.heads * a.ratio;
+  const int64_t mi = tok * heads + qhead;
+  if (a.out == nullptr) {
+    *reinterpret_cast<float4*>(a.mid + mi * D + d) = o;
+    if (d == 0) a.mid_lse[mi] = lse;
+    return;
+  }
+  if (a.mid != nullptr) {
+    const float4 p = __ldcg(reinterpret_cast<const float4*>(a.mid + mi * D + d));
+    const float pl = __ldcg(a.mid_lse + mi);
+    // A level that met nothing (lse = -inf) counts for nothing. fmaxf drops a NaN, which the
+    // weights below bring back.
+    const float top = fmaxf(lse, pl), ref = top == kNegInf ? 0.f : top;
+    float w0 = ex2(pl - ref), w1 = ex2(lse - ref);
+    const float inv = top == kNegInf ? 0.f : __frcp_rn(w0 + w1);
+    w0 *= inv;
+    w1 *= inv;
+    // a level of weight 0 keeps its values out (they may be anything if it met nothing)
+    o.x = (pl == kNegInf ? 0.f : w0 * p.x) + (lse == kNegInf ? 0.f : w1 * o.x);
+    o.y = (pl == kNegInf ? 0.f : w0 * p.y) + (lse == kNegInf ? 0.f : w1 * o.y);
+    o.z = (pl == kNegInf ? 0.f : w0 * p.z) + (lse == kNegInf ? 0.f : w1 * o.z);
+    o.w = (pl == kNegInf ? 0.f : w0 * p.w) + (lse == kNegInf ? 0.f : w1 * o.w);
+  }
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
+  uint2 v;
+  v.x = *reinterpret_cast<const uint32_t*>(&lo);
+  v.y = *reinterpret_cast<const uint32_t*>(&hi);
+  *reinterpret_cast<uint2*>(a.out + tok * a.ldo + static_cast<int64_t>(qhead) * D + d) = v;
+}
+
+template <int D, int BITS, int GROUP, int NT>
+__global__ void __launch_bounds__(kThreads)
+cache_attend_kernel(const Level a) {
+  using C = Cfg<D, BITS, GROUP, NT>;
+  constexpr int G = C::G, R = C::R, RB = C::RB;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ Find find;
+  __shared__ float row_m[kWarps][R], row_l[kWarps][R];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t me = blockIdx.x;
+  const Cut cut = find_tile<R>(a, me, find);
+  if (threadIdx.x == 0) a.join[me * 8] = 0;
+  if (me >= cut.parts || cut.total == 0) return;
+  const int64_t end = cut.begin(me + 1);
+  int64_t cur = cut.begin(me), b = find.b, base = find.base;
+  const int64_t sequences = a.fixed_len >= 0 ? 1 : a.rows.batch;
+  Sequence s = get_sequence<R>(a, b);
+
+  uint8_t* ring = smem + warp * C::kRing;
+  const uint32_t ring_addr = smem_u32(ring);
+
+  while (cur < end) {
+    // ---- the next run of tiles of one item ----
+    while (cur >= base + s.tiles) {
+      if (b + 1 >= sequences) return;   // only if the lengths changed under this kernel
+      base += s.tiles;
+      s = get_sequence<R>(a, ++b);
+    }
+    const int64_t rel = cur - base, item = rel / s.tiles_per, tile0 = rel - item * s.tiles_per;
+    const int head = static_cast<int>(item / s.row_tiles);
+    const int64_t row_first = (item - static_cast<int64_t>(head) * s.row_tiles) * R;
+    const int64_t run = min(s.tiles_per - tile0, end - cur);
+    const int32_t* table = a.rows.table + (a.fixed_len >= 0 ? 0 : b * a.rows.ld_table);
+    const int64_t tok_begin = tile0 * kTile;
+    const int64_t tok_end = min(s.len, (tile0 + run) * kTile);
+    // row j of the tile is token j / ratio, query head head * ratio + j % ratio; it meets positions
+    // below limit(j)
+    const int64_t n_rows = s.count * a.ratio;
+    auto limit_of = [&](int64_t j) -> int64_t {
+      if (j >= n_rows) return 0;
+      return a.fixed_len >= 0 ? s.len : s.len - s.end + s.row0 + j / a.ratio + 1;
+    };
+    // the lowest and highest limit of the tile's rows (limits ascend with the row)
+    const int64_t limit_lo = limit_of(row_first);
+    const int64_t limit_hi = limit_of(min(row_first + R, n_rows) - 1);
+
+    // ---- queries: this lane's dims of row g (and g + 8), fp16, scaled by a power of two ----
+    uint32_t qf[NT][D / 8];
+    float qsum[NT][G][2], row_scale[NT][2];
+    int lim[NT][2];                 // limits of rows 2t and 2t + 1, clamped to int
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int64_t j = row_first + nt * 8 + g;
+      constexpr int CPD = D / 4 / C::NPS;   // dims of a piece
+      constexpr int CH = CPD < 8 ? CPD : 8;
+      float x[D / 4];
+      if (j < n_rows) {
+        const int64_t tok = s.row0 + j / a.ratio;
+        const __nv_bfloat16* q =
+            a.q + tok * a.ldq + (static_cast<int64_t>(head) * a.ratio + j % a.ratio) * D;
+#pragma unroll
+        for (int p = 0; p < C::NPS; ++p)
+#pragma unroll
+          for (int e = 0; e < CPD; e += CH) {
+            const uint4 v = *reinterpret_cast<const uint4*>(q + (p * 4 + t) * CPD + e);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[p * CPD + e + 2 * i] = __uint_as_float(w[i] << 16);
+              x[p * CPD + e + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+          }
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
+      }
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // 2^(14 - e), e the exponent of the largest value (bounded so that both powers are normal)
+      const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
+      const float up = e > 127 ? 1.f : __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
+      const float down =
+          e > 127 ? 1.f : __uint_as_float(static_cast<uint32_t>(max(e - 14 + 127, 1)) << 23);
+      float sum[G];
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) sum[gr] = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 4; i += 8) {
+        // in the order that the codes of 32 bits (two words of 8-bit codes) come out of their words
+        float y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = x[i + k] * up;
+        uint32_t h[4];
+        if constexpr (BITS == 4) {
+          h[0] = half2_bits(y[0], y[4]);
+          h[1] = half2_bits(y[1] * 0.0625f, y[5] * 0.0625f);
+          h[2] = half2_bits(y[2], y[6]);
+          h[3] = half2_bits(y[3] * 0.0625f, y[7] * 0.0625f);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) h[k] = half2_bits(y[2 * k], y[2 * k + 1]);
+        }
+        constexpr int kPieceGroup = C::NPS / G;   // pieces per group
+        const int gr = i / CPD / kPieceGroup;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          qf[nt][i / 2 + k] = h[k];
+          const float2 f = half2_floats(h[k]);
+          sum[gr] = fmaf(BITS == 4 && (k & 1) ? 16.f : 1.f, f.x + f.y, sum[gr]);
+        }
+      }
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) {
+        sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 1);
+        sum[gr] += __shfl_xor_sync(0xffffffffu, sum[gr], 2);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)   // times the 2^-24 that the codes carry
+          qsum[nt][gr][k] = __shfl_sync(0xffffffffu, sum[gr], (2 * t + k) * 4) * 5.9604645e-8f;
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        row_scale[nt][k] =
+            __shfl_sync(0xffffffffu, down, (2 * t + k) * 4) * 16777216.f * a.scale_log2;
+        lim[nt][k] = static_cast<int>(
+            min(max(limit_of(row_first + nt * 8 + 2 * t + k), static_cast<int64_t>(0)), s.len));
+      }
+    }
+
+    float o[NT][D / 16][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        m[nt][k] = kNegInf;
+        l[nt][k] = 0.f;
+      }
+    }
+
+    // ---- this warp's steps: tokens tok_begin + 16 (warp + 4 i) ----
+    const int64_t stop = min(tok_end, limit_hi);   // no row meets anything behind
+    const int64_t first = tok_begin + kStep * warp;
+    const int steps = stop > first ? static_cast<int>((stop - first + kTile - 1) / kTile) : 0;
+    // pages of 32 steps, one per lane, and of the 32 after them
+    auto pages_from = [&](int i) -> int32_t {
+      const int k = i + lane;
+      return k < steps ? find_page(a.cache, table, first + static_cast<int64_t>(k) * kTile, a.info)
+                       : -1;
+    };
+    int32_t pages_now = pages_from(0), pages_next = steps > 32 ? pages_from(32) : -1;
+    int32_t pages_old = -1;
+
+    auto issue = [&](int i) {
+      if (i < steps) {
+        const int32_t page = __shfl_sync(0xffffffffu, pages_now, i & 31);
+        if (page >= 0) {
+          const int64_t pos = first + static_cast<int64_t>(i) * kTile;
+          const int64_t row = cache_row(a.cache, page, head,
+                                        static_cast<int>(pos) & ((1 << a.cache.page_shift) - 1));
+          const uint32_t st = ring_addr + (i % kStages) * C::kStage;
+          const uint8_t* k0 = a.cache.half[0].codes + row * RB;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int p = 0; p < C::NPS; ++p)
+              cp_async(st + ((h * C::NPS + p) * 32 + lane) * C::CPB,
+                       k0 + (g + 8 * h) * RB + (p * 4 + t) * C::CPB, C::CPB);
+          const uint8_t* v0 = a.cache.half[1].codes + row * RB;
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+              cp_async(st + C::kK + ((h * G + gr) * 32 + lane) * C::VB,
+                       v0 + (2 * t + (h & 1) + 8 * (h >> 1)) * RB + gr * (GROUP * BITS / 8) +
+                           (C::VGB < 4 ? (g >> 1) * 4 : g * C::VGB),
+                       C::VB);
+          // scales and zeros of the 16 tokens: 6 G pieces of 16 bytes
+          if (lane < 6 * G) {
+            const int half = lane >= 3 * G, e = lane - half * 3 * G;
+            const uint8_t* src =
+                e < 2 * G ? reinterpret_cast<const uint8_t*>(a.cache.half[half].scales + row * G) +
+                                16 * e
+                          : a.cache.half[half].zeros + row * G + 16 * (e - 2 * G);
+            cp_async(st + C::kK + C::kV + 16 * lane, src, 16);
+          }
+        }
+        if ((i & 31) == 31) {      // the next step's page is in the next batch
+          pages_old = pages_now;
+          pages_now = pages_next;
+          pages_next = pages_from(i + 33);
+        }
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+    for (int i = 0; i < steps; ++i) {
+      cp_wait<kStages - 2>();
+      __syncwarp();
+      const uint8_t* st = ring + (i % kStages) * C::kStage;
+      // step i's page: its batch is the one being issued from, or the one before
+      const int issued = i + kStages - 1;      // the next step to issue
+      const bool in_old = (min(issued, steps) >> 5) != (i >> 5);
+      const bool have =
+          __shfl_sync(0xffffffffu, in_old ? pages_old : pages_now, i & 31) >= 0;
+      const int pos = static_cast<int>(first + static_cast<int64_t>(i) * kTile);
+
+      // grids of tokens g and g + 8
+      float sk[2][G], nz[2][G], ratio_v[2][G], ls[2], rs[2];
+      const uint16_t* gk = reinterpret_cast<const uint16_t*>(st + C::kK + C::kV);
+      const uint8_t* zk = st + C::kK + C::kV + 32 * G;
+      const uint16_t* gv = reinterpret_cast<const uint16_t*>(st + C::kK + C::kV + 48 * G);
+      const uint8_t* zvp = st + C::kK + C::kV + 80 * G;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float top = kScaleFloor;
+        float sv[G];
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) {
+          const int at = (g + 8 * h) * G + gr;
+          sk[h][gr] = bf16_bits_to_float(gk[at]);
+          nz[h][gr] = -static_cast<float>(zk[at]);
+          sv[gr] = bf16_bits_to_float(gv[at]);
+          top = fmaxf(top, sv[gr]);
+        }
+        // the token's reference scale (its largest, at least 2^-96 so that sums of 1 / s stay
+        // finite) and each group's share of it
+        ls[h] = lg2(top);
+        rs[h] = __frcp_rn(top);
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr) ratio_v[h][gr] = sv[gr] * rs[h];
+      }
+
+      // ---- x: 16 tokens x 8 NT rows ----
+      float x[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[nt][e] = 0.f;
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) {
+        float c[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[nt][e] = 0.f;
+#pragma unroll
+        for (int pp = 0; pp < C::NPS / G; ++pp) {
+          const int p = gr * (C::NPS / G) + pp;
+          uint32_t wa[C::CPB / 4], wb[C::CPB / 4];
+          const uint8_t* pa = st + (p * 32 + lane) * C::CPB;
+          const uint8_t* pb = st + ((C::NPS + p) * 32 + lane) * C::CPB;
+          if constexpr (C::CPB == 16) {
+            *reinterpret_cast<uint4*>(wa) = *reinterpret_cast<const uint4*>(pa);
+            *reinterpret_cast<uint4*>(wb) = *reinterpret_cast<const uint4*>(pb);
+          } else if constexpr (C::CPB == 8) {
+            *reinterpret_cast<uint2*>(wa) = *reinterpret_cast<const uint2*>(pa);
+            *reinterpret_cast<uint2*>(wb) = *reinterpret_cast<const uint2*>(pb);
+          } else {
+            wa[0] = *reinterpret_cast<const uint32_t*>(pa);
+            wb[0] = *reinterpret_cast<const uint32_t*>(pb);
+          }
+#pragma unroll
+          for (int w = 0; w < C::CPB / 4; ++w) {
+            const int wi = p * (C::CPB / 4) + w;     // word of this lane's row
+            if constexpr (BITS == 4) {
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                const uint32_t u = hf ? wa[w] >> 8 : wa[w], v = hf ? wb[w] >> 8 : wb[w];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma_f16(c[nt], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u,
+                          v & 0x00F000F0u, qf[nt][4 * wi + 2 * hf], qf[nt][4 * wi + 2 * hf + 1]);
+              }
+            } else {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16(c[nt], __byte_perm(wa[w], 0, 0x4140), __byte_perm(wb[w], 0, 0x4140),
+                        __byte_perm(wa[w], 0, 0x4342), __byte_perm(wb[w], 0, 0x4342),
+                        qf[nt][2 * wi], qf[nt][2 * wi + 1]);
+            }
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[nt][e] = fmaf(sk[e >> 1][gr], fmaf(nz[e >> 1][gr], qsum[nt][gr][e & 1], c[nt][e]),
+                            x[nt][e]);
+      }
+
+      // ---- weights relative to the running reference M ----
+      const bool inner = have && pos + kStep <= limit_lo && row_first + R <= n_rows;
+      float p[NT][4];
+      bool above = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float u = fmaf(x[nt][e], row_scale[nt][e & 1], ls[e >> 1]);
+          if (!inner && !(have && pos + g + 8 * (e >> 1) < lim[nt][e & 1])) u = kNegInf;
+          p[nt][e] = u;
+          above |= u > m[nt][e & 1] + 8.f;
+        }
+      if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float top = fmaxf(m[nt][k], fmaxf(p[nt][k], p[nt][2 + k]));
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1)
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float f = m[nt][k] == kNegInf ? 0.f : ex2(m[nt][k] - top);
+            m[nt][k] = top;
+            l[nt][k] *= f;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+              o[nt][d][k] *= f;
+              o[nt][d][2 + k] *= f;
+            }
+          }
+      }
+      uint32_t bf[NT][G][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float ref = m[nt][e & 1];
+          const float w = ex2(p[nt][e] - (ref == kNegInf ? 0.f : ref));
+          // a masked token's grid may be anything (NaN too): its weight is 0 by selection
+          const bool on = inner || p[nt][e] != kNegInf;
+          l[nt][e & 1] += on ? w * rs[e >> 1] : 0.f;
+          p[nt][e] = on ? w : 0.f;
+        }
+#pragma unroll
+        for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float w0 = p[nt][2 * h] == 0.f ? 0.f : p[nt][2 * h] * ratio_v[h][gr];
+            const float w1 = p[nt][2 * h + 1] == 0.f ? 0.f : p[nt][2 * h + 1] * ratio_v[h][gr];
+            bf[nt][gr][h] = transpose8x8(half2_bits(w0, w1));
+          }
+      }
+
+      // ---- o: 16 dims x 8 NT rows per product ----
+#pragma unroll
+      for (int gr = 0; gr < G; ++gr) {
+        uint32_t w[4][C::VB / 4];
+        // zero points of tokens 2t and 2t + 1, and of the two eight further on, as fp16 codes
+        uint32_t zp[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t* z = zvp + (2 * t + 8 * h) * G + gr;
+          zp[h] = z[0] | static_cast<uint32_t>(z[G]) << 16;
+        }
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const uint8_t* pv = st + C::kK + ((h * G + gr) * 32 + lane) * C::VB;
+          if constexpr (C::VB == 16)
+            *reinterpret_cast<uint4*>(w[h]) = *reinterpret_cast<const uint4*>(pv);
+          else if constexpr (C::VB == 8)
+            *reinterpret_cast<uint2*>(w[h]) = *reinterpret_cast<const uint2*>(pv);
+          else
+            w[h][0] = *reinterpret_cast<const uint32_t*>(pv);
+          if constexpr (C::VGB < 4) w[h][0] >>= 16 * (g & 1);
+        }
+        constexpr int kPairs = BITS == 4 ? (C::VGB < 4 ? 2 : 4) : 2;   // dim pairs of a word
+#pragma unroll
+        for (int wi = 0; wi < C::VB / 4; ++wi) {
+          uint32_t ev[4], od[4];       // even and odd codes of the word, 4 bits: in bytes
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            ev[h] = BITS == 4 ? w[h][wi] & 0x0F0F0F0Fu : w[h][wi];
+            od[h] = BITS == 4 ? (w[h][wi] >> 4) & 0x0F0F0F0Fu : w[h][wi];
+          }
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) {
+            uint32_t a0, a1, a2, a3;
+            if constexpr (BITS == 4) {
+              const uint32_t sel = i | (8 | i) << 4 | (4 + i) << 8 | (8 | i) << 12;
+              a0 = prmt(ev[0], ev[1], sel);
+              a1 = prmt(od[0], od[1], sel);
+              a2 = prmt(ev[2], ev[3], sel);
+              a3 = prmt(od[2], od[3], sel);
+            } else {
+              const uint32_t s0 = (2 * i) | (4 + 2 * i) << 8, s1 = (2 * i + 1) | (5 + 2 * i) << 8;
+              a0 = prmt(ev[0], ev[1], s0) & 0x00FF00FFu;
+              a1 = prmt(od[0], od[1], s1) & 0x00FF00FFu;
+              a2 = prmt(ev[2], ev[3], s0) & 0x00FF00FFu;
+              a3 = prmt(od[2], od[3], s1) & 0x00FF00FFu;
+            }
+            a0 = sub_f16x2(a0, zp[0]);
+            a1 = sub_f16x2(a1, zp[0]);
+            a2 = sub_f16x2(a2, zp[1]);
+            a3 = sub_f16x2(a3, zp[1]);
+            const int tile = gr * (GROUP / 16) + wi * kPairs + i;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(o[nt][tile], a0, a1, a2, a3, bf[nt][gr][0], bf[nt][gr][1]);
+          }
+        }
+      }
+      __syncwarp();          // every lane is done with the stage that the next copies overwrite
+      issue(issued);
+    }
+    cp_wait<0>();
+
+    // ---- join the four warps ----
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], off);
+        }
+    __syncthreads();       // the rings are idle, and the last item's results have been read
+    float* res = reinterpret_cast<float*>(smem) + warp * R * C::kPad;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (g == 0) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r = nt * 8 + 2 * t + k;
+          row_m[warp][r] = m[nt][k];
+          row_l[warp][r] = l[nt][k];
+        }
+      }
+#pragma unroll
+      for (int tile = 0; tile < D / 16; ++tile) {
+        const int gr = tile / (GROUP / 16), i = tile % (GROUP / 16);
+        const int d = gr * GROUP + g * (GROUP / 8) + 2 * i;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          *reinterpret_cast<float2*>(res + (nt * 8 + 2 * t + k) * C::kPad + d) =
+              make_float2(o[nt][tile][k] * 16777216.f, o[nt][tile][2 + k] * 16777216.f);
+      }
+    }
+    __syncthreads();
+    const bool whole = run == s.tiles_per;
+    const int64_t slot = tile0 == 0 ? 2 * me + 1 : 2 * me;
+    for (int k = threadIdx.x; k < R * (D / 4); k += kThreads) {
+      const int r = k / (D / 4), d = k % (D / 4) * 4;
+      const int64_t j = row_first + r;
+      if (j >= n_rows) continue;
+      float top = kNegInf;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, row_m[w][r]);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float den = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        // a warp without a finite maximum met nothing, or only NaN (its sum is then NaN)
+        const float f = row_m[w][r] == kNegInf ? (row_l[w][r] == 0.f ? 0.f : 1.f)
+                                               : ex2(row_m[w][r] - top);
+        const float4 v = *reinterpret_cast<const float4*>(
+            reinterpret_cast<const float*>(smem) + (w * R + r) * C::kPad + d);
+        den = fmaf(f, row_l[w][r], den);
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+      const float inv = den == 0.f ? 0.f : 1.f / den;
+      acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      const float lse = den == 0.f ? kNegInf : (top == kNegInf ? 0.f : top) + log2f(den);
+      if (whole) {
+        finish<D>(a, s.row0 + j / a.ratio, head * a.ratio + static_cast<int>(j % a.ratio), d, acc,
+                  lse);
+      } else {
+        *reinterpret_cast<float4*>(a.part + (slot * R + r) * D + d) = acc;
+        if (d == 0) a.part_lse[slot * R + r] = lse;
+      }
+    }
+    if (!whole && tile0 == 0 && threadIdx.x == 0) {
+      // this run holds the item's beginning: runs me + 1 .. last hold the rest
+      const int64_t t_last = base + (item + 1) * s.tiles_per - 1;
+      int64_t last = me + 1;
+      while (last + 1 < cut.parts && cut.begin(last + 1) <= t_last) ++last;
+      int32_t* join = a.join + me * 8;
+      join[1] = static_cast<int32_t>(min(n_rows - row_first, static_cast<int64_t>(R)));
+      join[2] = head;
+      *reinterpret_cast<int64_t*>(join + 4) = s.row0;
+      *reinterpret_cast<int64_t*>(join + 6) = row_first;
+      join[0] = static_cast<int32_t>(last - me);
+    }
+    cur += run;
+  }
+}
+
+// Joins the partial results of the item that starts in run blockIdx.x and ends in a later one: slot
+// 2 c + 1 of its first run c, slots 2 c' of the runs after it. gridDim.y CTAs share the rows of the
+// item, so few long sequences still keep many SMs busy; the warps of a row share its slots.
+constexpr int kJoinWarps = 8;
+template <int D, int R>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+cache_join_kernel(const Level a) {
+  __shared__ float sh[kJoinWarps][D];
+  __shared__ float sh_m[kJoinWarps], sh_l[kJoinWarps];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t c = blockIdx.x;
+  const int32_t* join = a.join + c * 8;
+  const int runs = __ldcg(join);
+  if (runs == 0) return;
+  const int live = __ldcg(join + 1), head = __ldcg(join + 2);
+  const int64_t row0 = __ldcg(reinterpret_cast<const long long*>(join + 4));
+  const int64_t row_first = __ldcg(reinterpret_cast<const long long*>(join + 6));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows_here = R / gridDim.y;
+  const int per_row = max(1, kJoinWarps / rows_here);     // warps of a row
+  constexpr int kVec = D / 32;                            // dims of a lane: 2 or 4
+  for (int rr = warp / per_row; rr < rows_here; rr += kJoinWarps / per_row) {
+    const int r = blockIdx.y * rows_here + rr, sub = warp % per_row;
+    float m = kNegInf, l = 0.f, acc[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) acc[k] = 0.f;
+    auto add = [&](float lse, const float* v) {
+      if (lse == kNegInf) return;
+      const float top = fmaxf(m, lse), ref = top == kNegInf ? 0.f : top;
+      const float f = m == kNegInf ? (l == 0.f ? 0.f : 1.f) : ex2(m - ref), w = ex2(lse - ref);
+      m = top;
+      l = fmaf(l, f, w);
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) acc[k] = fmaf(acc[k], f, w * v[k]);
+    };
+    constexpr int kAhead = 8;
+    if (r < live) {
+      for (int s0 = sub; s0 <= runs; s0 += per_row * kAhead) {
+        float v[kAhead][kVec], lse[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int si = s0 + u * per_row;
+          lse[u] = kNegInf;
+          if (si > runs) continue;
+          const int64_t slot = si == 0 ? 2 * c + 1 : 2 * (c + si);
+          lse[u] = __ldcg(a.part_lse + slot * R + r);
+          const float* src = a.part + (slot * R + r) * D + lane * kVec;
+          if constexpr (kVec == 4)
+            *reinterpret_cast<float4*>(v[u]) = __ldcg(reinterpret_cast<const float4*>(src));
+          else
+            *reinterpret_cast<float2*>(v[u]) = __ldcg(reinterpret_cast<const float2*>(src));
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) add(lse[u], v[u]);
+      }
+    }
+    if (per_row > 1) {
+      // the loop runs once for every warp here: rows_here * per_row == kJoinWarps
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) sh[warp][lane * kVec + k] = acc[k];
+      if (lane == 0) {
+        sh_m[warp] = m;
+        sh_l[warp] = l;
+      }
+      __syncthreads();
+      if (sub == 0) {
+        for (int w = 1; w < per_row; ++w) {
+          const float wm = sh_m[warp + w], wl = sh_l[warp + w];
+          if (wm == kNegInf && wl == 0.f) continue;
+          const float top = fmaxf(m, wm), ref = top == kNegInf ? 0.f : top;
+          const float f = m == kNegInf ? (l == 0.f ? 0.f : 1.f) : ex2(m - ref);
+          const float g = wm == kNegInf ? 1.f : ex2(wm - ref);
+          m = top;
+          l = l * f + wl * g;
+#pragma unroll
+          for (int k = 0; k < kVec; ++k)
+            acc[k] = acc[k] * f + sh[warp + w][lane * kVec + k] * g;
+        }
+      }
+    }
+    if (sub == 0 && r < live) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float lse = l == 0.f ? kNegInf : (m == kNegInf ? 0.f : m) + log2f(l);
+      float x[4];
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) x[k] = acc[k] * inv;
+      const int64_t j = row_first + r;
+      const int64_t tok = row0 + j / a.ratio;
+      const int qhead = head * a.ratio + static_cast<int>(j % a.ratio);
+      if constexpr (kVec == 4) {
+        finish<D>(a, tok, qhead, lane * 4, make_float4(x[0], x[1], x[2], x[3]), lse);
+      } else {
+        x[2] = __shfl_down_sync(0xffffffffu, x[0], 1);
+        x[3] = __shfl_down_sync(0xffffffffu, x[1], 1);
+        if ((lane & 1) == 0)
+          finish<D>(a, tok, qhead, lane * 2, make_float4(x[0], x[1], x[2], x[3]), lse);
+      }
+    }
+  }
+}
+
+// CTAs of the attention kernel that fit on the device at once, cached per instance and device.
+template <int D, int BITS, int GROUP, int NT>
+int resident_ctas() {
+  static std::mutex mu;
+  static int cache[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (cache[dev] == 0) {
+    using C = Cfg<D, BITS, GROUP, NT>;
+    int per = 0;
+    const void* k = reinterpret_cast<const void*>(cache_attend_kernel<D, BITS, GROUP, NT>);
+    if (set_max_dynamic_smem(k, C::kSmem) != GPTQ_OK ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, k, kThreads, C::kSmem) != cudaSuccess ||
+        per <= 0)
+      return 0;
+    cache[dev] = std::min(per, kMaxResident) * num_sms();
+  }
+  return cache[dev];
+}
+
+template <int D, int BITS, int GROUP, int NT>
+gptq_status attend_level(Level a, cudaStream_t stream) {
+  using C = Cfg<D, BITS, GROUP, NT>;
+  const int resident = resident_ctas<D, BITS, GROUP, NT>();
+  if (resident <= 0) return GPTQ_ECUDA;
+  // no more runs than there can be tiles
+  const int64_t seqs = a.fixed_len >= 0 ? 1 : a.rows.batch;
+  const int64_t row_tiles = (a.rows.n * a.ratio + C::R - 1) / C::R + seqs;
+  const int64_t longest = a.fixed_len >= 0
+                              ? a.fixed_len
+                              : static_cast<int64_t>(a.cache.width) << a.cache.page_shift;
+  const int64_t per = std::max<int64_t>((longest + kTile - 1) / kTile, 1);
+  const int64_t items = row_tiles * a.cache.heads;
+  int64_t grid = resident;
+  if (items < resident && per < resident) grid = std::min<int64_t>(resident, items * per);
+  gptq_status st =
+      launch_pdl(cache_attend_kernel<D, BITS, GROUP, NT>, dim3(static_cast<unsigned>(grid)),
+                 dim3(kThreads), C::kSmem, stream, a);
+  if (st != GPTQ_OK || per == 1) return st;    // items of one tile are never shared
+  const unsigned y = items < num_sms() ? C::R : 1;
+  return launch_pdl(cache_join_kernel<D, C::R>, dim3(static_cast<unsigned>(grid), y),
+                    dim3(32 * kJoinWarps), 0, stream, a);
+}
+
+size_t slots_bytes(int dim) {
+  const size_t runs = static_cast<size_t>(num_sms()) * kMaxResident;
+  return align_up(runs * 8 * 4, 256) + align_up(2 * runs * 16 * 4, 256) +
+         align_up(2 * runs * 16 * static_cast<size_t>(dim) * 4, 256);
+}
+
+}  // namespace
+
+size_t cache_workspace_bytes(int heads, int dim, int64_t n, int ratio, bool shared) {
+  size_t b = slots_bytes(dim);
+  if (shared) {
+    const size_t rows = static_cast<size_t>(n) * heads * ratio;
+    b += align_up(rows * 4, 256) + align_up(rows * dim * 4, 256);
+  }
+  return b;
+}
+
+gptq_status run_cache_attend(const CacheView& c, const CacheRows& r, int dim, int bits, int group,
+                             const CacheQuery& q, void* ws, int32_t* info, cudaStream_t stream) {
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const size_t runs = static_cast<size_t>(num_sms()) * kMaxResident;
+  Level a{};
+  a.cache = c;
+  a.rows = r;
+  a.fixed_len = -1;
+  a.q = q.q;
+  a.ldq = q.ldq;
+  a.ratio = q.ratio;
+  a.scale_log2 = q.scale * 1.4426950408889634f;
+  a.out = q.out;
+  a.ldo = q.ldo;
+  a.info = info;
+  a.join = reinterpret_cast<int32_t*>(w);
+  w += align_up(runs * 8 * 4, 256);
+  a.part_lse = reinterpret_cast<float*>(w);
+  w += align_up(2 * runs * 16 * 4, 256);
+  a.part = reinterpret_cast<float*>(w);
+  w += align_up(2 * runs * 16 * static_cast<size_t>(dim) * 4, 256);
+  // 8 rows a tile where a sequence has no more on average, else 16: a second set of columns costs
+  // registers and products, a second pass over the codes costs more.
+  auto level = [&](const Level& l, int64_t rows_each) {
+    return dispatch_cache(dim, bits, group, [&](auto d, auto b, auto g) {
+      return rows_each <= 8 ? attend_level<d.value, b.value, g.value, 1>(l, stream)
+                            : attend_level<d.value, b.value, g.value, 2>(l, stream);
+    });
+  };
+  if (q.prefix_len > 0) {
+    const size_t rows = static_cast<size_t>(r.n) * c.heads * q.ratio;
+    a.mid_lse = reinterpret_cast<float*>(w);
+    a.mid = reinterpret_cast<float*>(w + align_up(rows * 4, 256));
+    Level p = a;
+    p.out = nullptr;
+    p.fixed_len = q.prefix_len;
+    p.rows.table = q.prefix_table;
+    p.cache.width = static_cast<int>((q.prefix_len + (1 << c.page_shift) - 1) >> c.page_shift);
+    const gptq_status st = level(p, r.n * q.ratio);
+    if (st != GPTQ_OK) return st;
+  }
+  return level(a, (r.n * q.ratio + r.batch - 1) / r.batch);
+}
+
+}  // namespace gptq
