@@ -277,25 +277,29 @@ def cache_rows(n, table, lengths, starts):
     """CacheRows of n rows: int32 tensors table [batch, width], lengths [batch] and starts
     [batch + 1] or None (row b is the last position of sequence b)."""
     import torch
-    for name, t in (("table", table), ("lengths", lengths), ("starts", starts)):
-        if t is not None and t.dtype != torch.int32:
-            raise TypeError(f"{name} must be int32")
-    ld = _row_major_ld(table, "table") if table.shape[1] > 1 else max(1, table.stride(0))
-    batch = table.shape[0]
-    for name, t, size in (("lengths", lengths, batch), ("starts", starts, batch + 1)):
-        if t is not None and (t.shape != (size,) or (size > 1 and t.stride(0) != 1)):
-            raise ValueError(f"{name} must be a dense vector of {size}")
-    return CacheRows(_ptr(table), max(ld, table.shape[1]), table.shape[1], _ptr(lengths),
-                     _ptr(starts), batch, int(n))
+    i32 = torch.int32
+    if table.dtype != i32 or lengths.dtype != i32 or (starts is not None and starts.dtype != i32):
+        raise TypeError("table, lengths and starts must be int32")
+    batch, width = table.shape
+    ld, unit = table.stride()
+    if (unit != 1 and width > 1) or (ld < width and batch > 1):
+        raise ValueError("table must have dense rows")
+    if lengths.shape != (batch,) or not lengths.is_contiguous():
+        raise ValueError(f"lengths must be a dense vector of {batch}")
+    if starts is not None and (starts.shape != (batch + 1,) or not starts.is_contiguous()):
+        raise ValueError(f"starts must be a dense vector of {batch + 1}")
+    return CacheRows(table.data_ptr(), ld if ld > width else width, width, lengths.data_ptr(),
+                     None if starts is None else starts.data_ptr(), batch, n)
 
 
 def _heads_ld(t, name, heads, dim):
     """Row stride of a [n, heads, dim] tensor whose rows are dense."""
-    if t.dim() != 3 or t.shape[1:] != (heads, dim):
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"{name} must be [n, {heads}, {dim}]")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+    if strides[2] != 1 or (heads > 1 and strides[1] != dim):
         raise ValueError(f"{name} must hold the heads of a row one after another")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * dim)
+    return strides[0] if shape[0] > 1 else max(strides[0], heads * dim)
 
 
 def _same_rows(t, like, name):

@@ -26,7 +26,6 @@ to it without unpacking it in memory:
 """
 from __future__ import annotations
 
-import contextlib
 from dataclasses import dataclass
 
 import torch
@@ -270,61 +269,66 @@ class QuantizedCache:
             setattr(self, name, t)
         self.pages, self.heads, self.page, self.dim = pages, heads, page, dim
         self.bits, self.group = 32 * words // dim, dim // groups
-        self.device = codes.device
+        self.device = codes.device      # with its index: a tensor's device always has one
         self.info = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._c = _lib.Cache(*(t.data_ptr() for t in tensors), pages, heads, page, dim, self.bits,
                              self.group)
 
-    @contextlib.contextmanager
-    def _on(self, stream, *tensors):
-        """The cache's device and the stream of the call, current for what the call allocates."""
+    def _run(self, stream, tensors, call):
+        """call(stream) with the cache's device and the call's stream current, for what the call
+        allocates; entered only where they are not current already."""
         for t in tensors:
             if t is not None and t.device != self.device:
                 raise ValueError(f"a tensor is on {t.device}, the cache on {self.device}")
+        if self.device.type != "cuda":
+            raise ValueError("the cache is not on a CUDA device")
+        if stream is None and torch.cuda.current_device() == self.device.index:
+            return call(torch._C._cuda_getCurrentRawStream(self.device.index))
         with torch.cuda.device(self.device):
             if stream is None:
-                yield torch.cuda.current_stream()
-                return
+                return call(None)
             if not isinstance(stream, torch.cuda.Stream):
                 stream = torch.cuda.ExternalStream(int(stream), self.device)
             with torch.cuda.stream(stream):
-                yield stream
+                return call(stream)
 
     def append(self, K, V, table, lengths, starts=None, K_hat=None, V_hat=None, stream=None):
         """Quantizes the rows K, V [n, heads, dim] (bf16 or fp32) into their positions. K_hat and
         V_hat, if given, receive what the cache now holds of them, s (q - z)."""
-        with self._on(stream, K, V, table, lengths, starts, K_hat, V_hat) as s:
-            _lib.cache_append(self._c, _lib.cache_rows(K.shape[0], table, lengths, starts), K, V,
-                              K_hat, V_hat, self.info, s)
+        self._run(stream, (K, V, table, lengths, starts, K_hat, V_hat), lambda s: _lib.cache_append(
+            self._c, _lib.cache_rows(K.shape[0], table, lengths, starts), K, V, K_hat, V_hat,
+            self.info, s))
 
     def read(self, table, lengths, starts=None, n=None, dtype=torch.bfloat16, K_out=None,
              V_out=None, stream=None):
         """The values of the rows' positions, (K, V) [n, heads, dim]; n as the outputs given, or
         as asked for (default: one row per sequence)."""
-        with self._on(stream, table, lengths, starts, K_out, V_out) as s:
-            like = K_out if K_out is not None else V_out
-            if like is None:
-                n = table.shape[0] if n is None else int(n)
-                K_out = torch.empty(n, self.heads, self.dim, dtype=dtype, device=self.device)
-                V_out = torch.empty_like(K_out)
-                like = K_out
-            _lib.cache_read(self._c, _lib.cache_rows(like.shape[0], table, lengths, starts),
-                            K_out, V_out, self.info, s)
-            return K_out, V_out
+        def call(s):
+            k, v = K_out, V_out
+            if k is None and v is None:
+                rows = table.shape[0] if n is None else int(n)
+                k = torch.empty(rows, self.heads, self.dim, dtype=dtype, device=self.device)
+                v = torch.empty_like(k)
+            rows = (v if k is None else k).shape[0]
+            _lib.cache_read(self._c, _lib.cache_rows(rows, table, lengths, starts), k, v,
+                            self.info, s)
+            return k, v
+        return self._run(stream, (table, lengths, starts, K_out, V_out), call)
 
     def _attend(self, Q, table, lengths, starts, scale, out, stream, prefix_table, prefix_len):
-        with self._on(stream, Q, table, lengths, starts, out, prefix_table) as s:
-            if Q.dim() != 3 or Q.shape[1] % self.heads or not Q.shape[1]:
-                raise ValueError(f"Q must be [n, k * {self.heads}, {self.dim}]")
-            ratio = Q.shape[1] // self.heads
-            if out is None:
-                out = torch.empty(Q.shape, dtype=Q.dtype, device=self.device)
-            size = _lib.cache_workspace_size(self._c, Q.shape[0], ratio, prefix_len is not None)
+        if Q.dim() != 3 or not Q.shape[1] or Q.shape[1] % self.heads:
+            raise ValueError(f"Q must be [n, k * {self.heads}, {self.dim}]")
+        n, ratio = Q.shape[0], Q.shape[1] // self.heads
+
+        def call(s):
+            o = torch.empty(Q.shape, dtype=Q.dtype, device=self.device) if out is None else out
+            size = _lib.cache_workspace_size(self._c, n, ratio, prefix_len is not None)
             ws = torch.empty(size, dtype=torch.uint8, device=self.device)
-            _lib.cache_attend(self._c, _lib.cache_rows(Q.shape[0], table, lengths, starts), Q, out,
-                              ratio, self.dim ** -0.5 if scale is None else scale, ws, self.info,
-                              s, prefix_table, prefix_len)
-            return out
+            _lib.cache_attend(self._c, _lib.cache_rows(n, table, lengths, starts), Q, o, ratio,
+                              self.dim ** -0.5 if scale is None else scale, ws, self.info, s,
+                              prefix_table, prefix_len)
+            return o
+        return self._run(stream, (Q, table, lengths, starts, out, prefix_table), call)
 
     def attend(self, Q, table, lengths, starts=None, scale=None, out=None, stream=None):
         """Causal softmax attention of Q [n, q_heads, dim] (bf16; q_heads a multiple of heads) over
