@@ -93,8 +93,8 @@ def attend_bound(q, kc, ks, kz, vc, vs, vz, scale: float, image16: bool = False)
       fp16 images of s (code - z), off by 2^-12 each: x_t moves by 2^-12 scale sum |q k| more. A
       relative error e of the weights moves the result by at most 2 e sum p |v|.
     * Each weight is rounded to fp16: by 2^-12 of itself, or by 2^-25 of the unit in which the
-      largest is at least 1. With `image16` each value is too, by 2^-12 of itself or 2^-36 of the
-      largest.
+      largest is at least 1. With `image16` each value is too, by 2^-12 of itself or 2^-32 of the
+      largest (key images likewise).
     * The sum over tokens runs in steps of 16 and is joined from parts: (tokens / 16 + 64) 2^-22 of
       sum p |v|.
     * The result is rounded to bf16: half a step, 2^-8 of the value that is rounded.
@@ -116,9 +116,10 @@ def attend_bound(q, kc, ks, kz, vc, vs, vz, scale: float, image16: bool = False)
     e = (dim / 16 + 8) * 2.0 ** -22 * A.max() + 2.0 ** -20
     steps = (T / 16 + 64) * 2.0 ** -22
     if image16:
-        e += 2.0 ** -12 * scale * (np.abs(k) @ np.abs(q)).max()
+        e += 2.0 ** -12 * scale * (np.abs(k) @ np.abs(q)).max() + \
+            2.0 ** -32 * scale * np.abs(k).max() * np.abs(q).sum()
         bound = mass * (2 * e + 2.0 ** -11 + steps) + \
-            2.0 ** -25 * p.max() * np.abs(v).sum(0) + 2.0 ** -36 * np.abs(v).max()
+            2.0 ** -25 * p.max() * np.abs(v).sum(0) + 2.0 ** -32 * np.abs(v).max()
     else:
         unit = (p[:, None] * vs.astype(np.float64)).max()
         z = np.repeat(vz.astype(np.float64), dim // G, 1)

@@ -372,6 +372,8 @@ static gptq_status attend_checked(const gptq_cache* cache, const gptq_cache_rows
   if (ratio < 1 || ratio > 1024) return GPTQ_EINVAL;
   const int64_t width = static_cast<int64_t>(cache->heads) * ratio * cache->dim;
   if ((st = check_rows(rows, width, &c, &r)) != GPTQ_OK) return st;
+  if (cache->heads * static_cast<int64_t>(ratio) > (1 << 18) || r.n * ratio > INT32_MAX)
+    return GPTQ_EUNSUPPORTED;
   if (ldq < width || ldo < width || ldq % 8 != 0 || ldo % 8 != 0) return GPTQ_EINVAL;
   if (!(scale >= -1e30f && scale <= 1e30f)) return GPTQ_EINVAL;
   if (prefix_len < 0) return GPTQ_EINVAL;

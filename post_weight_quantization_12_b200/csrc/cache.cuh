@@ -108,6 +108,11 @@ struct CacheQuery {
   const int32_t* prefix_table;
   int64_t prefix_len;
 };
+size_t prefix_workspace_bytes(int heads, int dim, int64_t n, int ratio);
+// The prefix on the tensor cores, joined with each row's own level (mid, mid_lse) into the output.
+gptq_status run_cache_prefix(const CacheView& c, const CacheRows& r, int dim, int bits, int group,
+                             const CacheQuery& q, const float* mid, const float* mid_lse, void* ws,
+                             int32_t* info, cudaStream_t stream);
 size_t cache_workspace_bytes(int heads, int dim, int64_t n, int ratio, bool shared);
 gptq_status run_cache_attend(const CacheView& c, const CacheRows& r, int dim, int bits, int group,
                              const CacheQuery& q, void* ws, int32_t* info, cudaStream_t stream);

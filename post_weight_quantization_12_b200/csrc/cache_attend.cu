@@ -39,7 +39,7 @@ namespace {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStep = 16;                   // tokens of one warp step
 constexpr int kTile = kStep * kWarps;       // tokens of one tile of work
-constexpr int kStages = 4;                  // ring depth of a warp, in steps
+constexpr int kStages = 3;                  // ring depth of a warp, in steps
 constexpr int kMaxResident = 4;             // CTAs per SM
 constexpr float kScaleFloor = 1.2621774e-29f;   // 2^-96, see below
 constexpr float kNegInf = -INFINITY;
@@ -85,37 +85,41 @@ struct Level {
 };
 
 struct Sequence {
-  int64_t row0, end;            // rows row0 .. row0 + count - 1; end: the nominal end
-  int64_t count, len, tiles;    // tiles of the whole sequence over all heads
-  int row_tiles;
-  int64_t tiles_per;            // of one (head, row tile)
+  int row0, end;                // rows row0 .. row0 + count - 1; end: the nominal end
+  int count, len;
+  int row_tiles, tiles_per;     // tiles of one (head, row tile)
+  int64_t tiles;                // of the sequence over all heads
 };
 
+// (The host admits fewer than 2^31 rows n * ratio, and lengths are int32: an item's own numbers
+// fit in 32 bits.)
 template <int R>
 __device__ __forceinline__ Sequence get_sequence(const Level& a, int64_t b) {
   Sequence s;
+  const int n = static_cast<int>(a.rows.n);
   if (a.fixed_len >= 0) {
     s.row0 = 0;
-    s.end = s.count = a.rows.n;
-    s.len = a.fixed_len;
+    s.end = s.count = n;
+    s.len = static_cast<int>(a.fixed_len);
   } else {
-    s.row0 = b;
-    s.end = b + 1;
+    s.row0 = static_cast<int>(b);
+    s.end = s.row0 + 1;
     if (a.rows.starts != nullptr) {
       s.row0 = max(__ldg(a.rows.starts + b), 0);
       s.end = __ldg(a.rows.starts + b + 1);
     }
-    s.count = max(min(s.end, a.rows.n) - s.row0, static_cast<int64_t>(0));
+    s.count = max(min(s.end, n) - s.row0, 0);
     s.len = __ldg(a.rows.lengths + b);
   }
   const int64_t cap = static_cast<int64_t>(a.cache.width) << a.cache.page_shift;
   if (s.len < 0 || s.len > cap) {
     if (threadIdx.x == 0) record_info(a.info, GPTQ_INFO_BAD_PAGE);
-    s.len = s.len < 0 ? 0 : cap;
+    s.len = s.len < 0 ? 0 : static_cast<int>(cap);
   }
-  s.row_tiles = static_cast<int>((s.count * a.ratio + R - 1) / R);
-  s.tiles_per = max((s.len + kTile - 1) / kTile, static_cast<int64_t>(1));
-  s.tiles = s.tiles_per * s.row_tiles * a.cache.heads;
+  s.row_tiles = (s.count * a.ratio + R - 1) / R;
+  s.tiles_per = max((s.len >> 6) + ((s.len & 63) != 0), 1);
+  static_assert(kTile == 64, "tiles_per");
+  s.tiles = static_cast<int64_t>(s.tiles_per) * s.row_tiles * a.cache.heads;
   return s;
 }
 
@@ -214,6 +218,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float lg2(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -262,8 +271,53 @@ __device__ __forceinline__ void finish(const Level& a, int64_t tok, int qhead, i
   *reinterpret_cast<uint2*>(a.out + tok * a.ldo + static_cast<int64_t>(qhead) * D + d) = v;
 }
 
+// One step's weights from its products: u = x c + log2(s) per token and row, the running reference
+// M, and 2^(u - M) in p. kEdge: some token does not count for some row (u = -inf there).
+template <int D, int NT, bool kEdge>
+__device__ __forceinline__ void weigh(float (&p)[NT][4], float (&m)[NT][2], float (&l)[NT][2],
+                                      float (&o)[NT][D / 16][4], const float (&rs)[2],
+                                      const bool (&on)[NT][4]) {
+  bool above = false;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (kEdge && !on[nt][e]) p[nt][e] = kNegInf;
+      above |= p[nt][e] > m[nt][e & 1] + 8.f;
+    }
+  if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float top = fmaxf(m[nt][k], fmaxf(p[nt][k], p[nt][2 + k]));
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1)
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float f = m[nt][k] == kNegInf ? 0.f : ex2(m[nt][k] - top);
+        m[nt][k] = top;
+        l[nt][k] *= f;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          o[nt][d][k] *= f;
+          o[nt][d][2 + k] *= f;
+        }
+      }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float ref = m[nt][e & 1];
+      const float w = ex2(p[nt][e] - (kEdge && ref == kNegInf ? 0.f : ref));
+      // a token that does not count may have any grid (NaN too): out by selection
+      p[nt][e] = kEdge && !on[nt][e] ? 0.f : w;
+      l[nt][e & 1] = kEdge && !on[nt][e] ? l[nt][e & 1] : fmaf(w, rs[e >> 1], l[nt][e & 1]);
+    }
+}
+
 template <int D, int BITS, int GROUP, int NT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
 cache_attend_kernel(const Level a) {
   using C = Cfg<D, BITS, GROUP, NT>;
   constexpr int G = C::G, R = C::R, RB = C::RB;
@@ -279,67 +333,146 @@ cache_attend_kernel(const Level a) {
   if (threadIdx.x == 0) a.join[me * 8] = 0;
   if (me >= cut.parts || cut.total == 0) return;
   const int64_t end = cut.begin(me + 1);
-  int64_t cur = cut.begin(me), b = find.b, base = find.base;
+  int64_t cur = cut.begin(me), b = find.b;
   const int64_t sequences = a.fixed_len >= 0 ? 1 : a.rows.batch;
   Sequence s = get_sequence<R>(a, b);
+  // the item that tile `cur` lies in, its first tile and the tile within it
+  int head, rt, tile0;
+  int64_t item0;
+  {
+    const int64_t rel = cur - find.base;
+    int64_t item;
+    if (rel >> 32) {
+      item = rel / s.tiles_per;
+      tile0 = static_cast<int>(rel - item * s.tiles_per);
+    } else {
+      const uint32_t q = static_cast<uint32_t>(rel) / static_cast<uint32_t>(s.tiles_per);
+      tile0 = static_cast<int>(static_cast<uint32_t>(rel) - q * s.tiles_per);
+      item = q;
+    }
+    head = static_cast<int>(item >> 32 ? item / s.row_tiles
+                                       : static_cast<uint32_t>(item) /
+                                             static_cast<uint32_t>(s.row_tiles));
+    rt = static_cast<int>(item - static_cast<int64_t>(head) * s.row_tiles);
+    item0 = cur - tile0;
+  }
 
   uint8_t* ring = smem + warp * C::kRing;
   const uint32_t ring_addr = smem_u32(ring);
+  // what this lane copies of 16 tokens, from the row of the first
+  const uint8_t* k_src = a.cache.half[0].codes + g * RB + t * C::CPB;
+  const uint8_t* v_src = a.cache.half[1].codes + 2 * t * RB +
+                         (C::VGB < 4 ? (g >> 1) * 4 : g * C::VGB);
+  // scales and zeros of the 16 tokens: 6 G pieces of 16 bytes, a lane a piece
+  const bool grid_lane = lane < 6 * G;
+  const uint8_t* g_src;
+  int g_row;                    // bytes of a token
+  {
+    const int half = lane >= 3 * G, e = lane - half * 3 * G;
+    g_row = e < 2 * G ? 2 * G : G;
+    g_src = e < 2 * G ? reinterpret_cast<const uint8_t*>(a.cache.half[half].scales) + 16 * e
+                      : a.cache.half[half].zeros + 16 * (e - 2 * G);
+  }
 
   while (cur < end) {
-    // ---- the next run of tiles of one item ----
-    while (cur >= base + s.tiles) {
-      if (b + 1 >= sequences) return;   // only if the lengths changed under this kernel
-      base += s.tiles;
-      s = get_sequence<R>(a, ++b);
-    }
-    const int64_t rel = cur - base, item = rel / s.tiles_per, tile0 = rel - item * s.tiles_per;
-    const int head = static_cast<int>(item / s.row_tiles);
-    const int64_t row_first = (item - static_cast<int64_t>(head) * s.row_tiles) * R;
-    const int64_t run = min(s.tiles_per - tile0, end - cur);
+    // ---- a run of tiles of one item ----
+    const int run = static_cast<int>(min(static_cast<int64_t>(s.tiles_per - tile0), end - cur));
+    const int row_first = rt * R;
     const int32_t* table = a.rows.table + (a.fixed_len >= 0 ? 0 : b * a.rows.ld_table);
-    const int64_t tok_begin = tile0 * kTile;
-    const int64_t tok_end = min(s.len, (tile0 + run) * kTile);
+    const int tok_begin = tile0 * kTile;
+    const int n_rows = s.count * a.ratio;
     // row j of the tile is token j / ratio, query head head * ratio + j % ratio; it meets positions
-    // below limit(j)
-    const int64_t n_rows = s.count * a.ratio;
-    auto limit_of = [&](int64_t j) -> int64_t {
+    // below limit_of(j), which ascends with j
+    auto limit_of = [&](int j) -> int {
       if (j >= n_rows) return 0;
-      return a.fixed_len >= 0 ? s.len : s.len - s.end + s.row0 + j / a.ratio + 1;
+      if (a.fixed_len >= 0) return s.len;
+      return min(max(s.len - s.end + s.row0 + static_cast<int>(static_cast<uint32_t>(j) /
+                                                               static_cast<uint32_t>(a.ratio)) + 1,
+                     0), s.len);
     };
-    // the lowest and highest limit of the tile's rows (limits ascend with the row)
-    const int64_t limit_lo = limit_of(row_first);
-    const int64_t limit_hi = limit_of(min(row_first + R, n_rows) - 1);
+    // (a tile's rows past the last one meet whatever the others do; their results are dropped)
+    const int limit_lo = limit_of(row_first);
+    const int limit_hi = limit_of(min(row_first + R, n_rows) - 1);
+
+    // ---- this warp's steps: tokens first + 64 i, and the pages of 32 of them, one per lane ----
+    const int stop = static_cast<int>(
+        min(static_cast<int64_t>(limit_hi), (static_cast<int64_t>(tile0) + run) * kTile));
+    const int first = tok_begin + kStep * warp;
+    const int steps = stop > first ? (stop - first + kTile - 1) / kTile : 0;
+    auto pages_from = [&](int i) -> int32_t {
+      const int k = i + lane;
+      return k < steps ? find_page(a.cache, table, first + static_cast<int64_t>(k) * kTile, a.info)
+                       : -1;
+    };
+    int32_t pages_now = pages_from(0), pages_next = steps > 32 ? pages_from(32) : -1;
+    int32_t pages_old = -1;
+
+    // the queries' loads go out while the pages come in
+    constexpr int CPD = D / 4 / C::NPS;   // dims of a piece
+    uint4 q_raw[NT][D / 32];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int j = row_first + nt * 8 + g;
+      const uint32_t tk = static_cast<uint32_t>(j) / static_cast<uint32_t>(a.ratio);
+      const __nv_bfloat16* q =
+          a.q + (s.row0 + static_cast<int64_t>(tk)) * a.ldq +
+          (static_cast<int64_t>(head) * a.ratio + (j - static_cast<int>(tk) * a.ratio)) * D;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i)
+        q_raw[nt][i] = j < n_rows ? __ldg(reinterpret_cast<const uint4*>(
+                                        q + (i * 8 / CPD * 4 + t) * CPD + i * 8 % CPD))
+                                  : make_uint4(0, 0, 0, 0);
+    }
+
+    uint32_t put = ring_addr;             // the stage that is filled next
+    auto issue = [&](int i) {
+      if (i < steps) {
+        const int32_t page = __shfl_sync(0xffffffffu, pages_now, i & 31);
+        if (page >= 0) {
+          const int off = (first + i * kTile) & ((1 << a.cache.page_shift) - 1);
+          const int64_t row = cache_row(a.cache, page, head, off);
+          const uint8_t* k0 = k_src + row * RB;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int p = 0; p < C::NPS; ++p)
+              cp_async(put + lane * C::CPB + (h * C::NPS + p) * 32 * C::CPB,
+                       k0 + 8 * h * RB + p * 4 * C::CPB, C::CPB);
+          const uint8_t* v0 = v_src + row * RB;
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+              cp_async(put + lane * C::VB + C::kK + (h * G + gr) * 32 * C::VB,
+                       v0 + ((h & 1) + 8 * (h >> 1)) * RB + gr * (GROUP * BITS / 8), C::VB);
+          if (grid_lane) cp_async(put + C::kK + C::kV + 16 * lane, g_src + row * g_row, 16);
+        }
+        put = put + C::kStage == ring_addr + C::kRing ? ring_addr : put + C::kStage;
+        if ((i & 31) == 31) {      // the next step's page is in the next batch
+          pages_old = pages_now;
+          pages_now = pages_next;
+          pages_next = pages_from(i + 33);
+        }
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
 
     // ---- queries: this lane's dims of row g (and g + 8), fp16, scaled by a power of two ----
     uint32_t qf[NT][D / 8];
     float qsum[NT][G][2], row_scale[NT][2];
-    int lim[NT][2];                 // limits of rows 2t and 2t + 1, clamped to int
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int64_t j = row_first + nt * 8 + g;
-      constexpr int CPD = D / 4 / C::NPS;   // dims of a piece
-      constexpr int CH = CPD < 8 ? CPD : 8;
       float x[D / 4];
-      if (j < n_rows) {
-        const int64_t tok = s.row0 + j / a.ratio;
-        const __nv_bfloat16* q =
-            a.q + tok * a.ldq + (static_cast<int64_t>(head) * a.ratio + j % a.ratio) * D;
 #pragma unroll
-        for (int p = 0; p < C::NPS; ++p)
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t w[4] = {q_raw[nt][i].x, q_raw[nt][i].y, q_raw[nt][i].z, q_raw[nt][i].w};
 #pragma unroll
-          for (int e = 0; e < CPD; e += CH) {
-            const uint4 v = *reinterpret_cast<const uint4*>(q + (p * 4 + t) * CPD + e);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x[p * CPD + e + 2 * i] = __uint_as_float(w[i] << 16);
-              x[p * CPD + e + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            }
-          }
-      } else {
-#pragma unroll
-        for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
+        for (int k = 0; k < 4; ++k) {
+          x[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
+          x[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+        }
       }
       float top = 0.f;
 #pragma unroll
@@ -370,8 +503,7 @@ cache_attend_kernel(const Level a) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) h[k] = half2_bits(y[2 * k], y[2 * k + 1]);
         }
-        constexpr int kPieceGroup = C::NPS / G;   // pieces per group
-        const int gr = i / CPD / kPieceGroup;
+        const int gr = i / CPD / (C::NPS / G);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           qf[nt][i / 2 + k] = h[k];
@@ -388,12 +520,9 @@ cache_attend_kernel(const Level a) {
           qsum[nt][gr][k] = __shfl_sync(0xffffffffu, sum[gr], (2 * t + k) * 4) * 5.9604645e-8f;
       }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < 2; ++k)
         row_scale[nt][k] =
             __shfl_sync(0xffffffffu, down, (2 * t + k) * 4) * 16777216.f * a.scale_log2;
-        lim[nt][k] = static_cast<int>(
-            min(max(limit_of(row_first + nt * 8 + 2 * t + k), static_cast<int64_t>(0)), s.len));
-      }
     }
 
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
@@ -410,81 +539,21 @@ cache_attend_kernel(const Level a) {
       }
     }
 
-    // ---- this warp's steps: tokens tok_begin + 16 (warp + 4 i) ----
-    const int64_t stop = min(tok_end, limit_hi);   // no row meets anything behind
-    const int64_t first = tok_begin + kStep * warp;
-    const int steps = stop > first ? static_cast<int>((stop - first + kTile - 1) / kTile) : 0;
-    // pages of 32 steps, one per lane, and of the 32 after them
-    auto pages_from = [&](int i) -> int32_t {
-      const int k = i + lane;
-      return k < steps ? find_page(a.cache, table, first + static_cast<int64_t>(k) * kTile, a.info)
-                       : -1;
-    };
-    int32_t pages_now = pages_from(0), pages_next = steps > 32 ? pages_from(32) : -1;
-    int32_t pages_old = -1;
-
-    auto issue = [&](int i) {
-      if (i < steps) {
-        const int32_t page = __shfl_sync(0xffffffffu, pages_now, i & 31);
-        if (page >= 0) {
-          const int64_t pos = first + static_cast<int64_t>(i) * kTile;
-          const int64_t row = cache_row(a.cache, page, head,
-                                        static_cast<int>(pos) & ((1 << a.cache.page_shift) - 1));
-          const uint32_t st = ring_addr + (i % kStages) * C::kStage;
-          const uint8_t* k0 = a.cache.half[0].codes + row * RB;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int p = 0; p < C::NPS; ++p)
-              cp_async(st + ((h * C::NPS + p) * 32 + lane) * C::CPB,
-                       k0 + (g + 8 * h) * RB + (p * 4 + t) * C::CPB, C::CPB);
-          const uint8_t* v0 = a.cache.half[1].codes + row * RB;
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-#pragma unroll
-            for (int gr = 0; gr < G; ++gr)
-              cp_async(st + C::kK + ((h * G + gr) * 32 + lane) * C::VB,
-                       v0 + (2 * t + (h & 1) + 8 * (h >> 1)) * RB + gr * (GROUP * BITS / 8) +
-                           (C::VGB < 4 ? (g >> 1) * 4 : g * C::VGB),
-                       C::VB);
-          // scales and zeros of the 16 tokens: 6 G pieces of 16 bytes
-          if (lane < 6 * G) {
-            const int half = lane >= 3 * G, e = lane - half * 3 * G;
-            const uint8_t* src =
-                e < 2 * G ? reinterpret_cast<const uint8_t*>(a.cache.half[half].scales + row * G) +
-                                16 * e
-                          : a.cache.half[half].zeros + row * G + 16 * (e - 2 * G);
-            cp_async(st + C::kK + C::kV + 16 * lane, src, 16);
-          }
-        }
-        if ((i & 31) == 31) {      // the next step's page is in the next batch
-          pages_old = pages_now;
-          pages_now = pages_next;
-          pages_next = pages_from(i + 33);
-        }
-      }
-      cp_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(i);
-
+    const uint8_t* st = ring;             // the stage that is consumed
     for (int i = 0; i < steps; ++i) {
       cp_wait<kStages - 2>();
       __syncwarp();
-      const uint8_t* st = ring + (i % kStages) * C::kStage;
       // step i's page: its batch is the one being issued from, or the one before
       const int issued = i + kStages - 1;      // the next step to issue
       const bool in_old = (min(issued, steps) >> 5) != (i >> 5);
       const bool have =
           __shfl_sync(0xffffffffu, in_old ? pages_old : pages_now, i & 31) >= 0;
-      const int pos = static_cast<int>(first + static_cast<int64_t>(i) * kTile);
+      const int pos = first + i * kTile;
 
       // grids of tokens g and g + 8
       float sk[2][G], nz[2][G], ratio_v[2][G], ls[2], rs[2];
-      const uint16_t* gk = reinterpret_cast<const uint16_t*>(st + C::kK + C::kV);
-      const uint8_t* zk = st + C::kK + C::kV + 32 * G;
-      const uint16_t* gv = reinterpret_cast<const uint16_t*>(st + C::kK + C::kV + 48 * G);
-      const uint8_t* zvp = st + C::kK + C::kV + 80 * G;
+      const uint8_t* grids = st + C::kK + C::kV;
+      const uint8_t* zvp = grids + 80 * G;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float top = kScaleFloor;
@@ -492,15 +561,15 @@ cache_attend_kernel(const Level a) {
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
           const int at = (g + 8 * h) * G + gr;
-          sk[h][gr] = bf16_bits_to_float(gk[at]);
-          nz[h][gr] = -static_cast<float>(zk[at]);
-          sv[gr] = bf16_bits_to_float(gv[at]);
+          sk[h][gr] = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(grids)[at]);
+          nz[h][gr] = -static_cast<float>((grids + 32 * G)[at]);
+          sv[gr] = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(grids + 48 * G)[at]);
           top = fmaxf(top, sv[gr]);
         }
         // the token's reference scale (its largest, at least 2^-96 so that sums of 1 / s stay
         // finite) and each group's share of it
         ls[h] = lg2(top);
-        rs[h] = __frcp_rn(top);
+        rs[h] = rcp(top);
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) ratio_v[h][gr] = sv[gr] * rs[h];
       }
@@ -564,58 +633,50 @@ cache_attend_kernel(const Level a) {
       }
 
       // ---- weights relative to the running reference M ----
-      const bool inner = have && pos + kStep <= limit_lo && row_first + R <= n_rows;
       float p[NT][4];
-      bool above = false;
+      bool on[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float u = fmaf(x[nt][e], row_scale[nt][e & 1], ls[e >> 1]);
-          if (!inner && !(have && pos + g + 8 * (e >> 1) < lim[nt][e & 1])) u = kNegInf;
-          p[nt][e] = u;
-          above |= u > m[nt][e & 1] + 8.f;
+          p[nt][e] = fmaf(x[nt][e], row_scale[nt][e & 1], ls[e >> 1]);
+          on[nt][e] = true;
         }
-      if (__any_sync(0xffffffffu, above)) {
+      uint32_t bf[NT][G][2];
+      if (have && pos + kStep <= limit_lo) {
+        weigh<D, NT, false>(p, m, l, o, rs, on);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float top = fmaxf(m[nt][k], fmaxf(p[nt][k], p[nt][2 + k]));
+          for (int gr = 0; gr < G; ++gr)
 #pragma unroll
-            for (int off = 4; off < 32; off <<= 1)
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            const float f = m[nt][k] == kNegInf ? 0.f : ex2(m[nt][k] - top);
-            m[nt][k] = top;
-            l[nt][k] *= f;
+            for (int h = 0; h < 2; ++h)
+              bf[nt][gr][h] = half2_bits(p[nt][2 * h] * ratio_v[h][gr],
+                                         p[nt][2 * h + 1] * ratio_v[h][gr]);
+      } else {
 #pragma unroll
-            for (int d = 0; d < D / 16; ++d) {
-              o[nt][d][k] *= f;
-              o[nt][d][2 + k] *= f;
-            }
-          }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            on[nt][e] = have && pos + g + 8 * (e >> 1) <
+                                    limit_of(row_first + nt * 8 + 2 * t + (e & 1));
+        weigh<D, NT, true>(p, m, l, o, rs, on);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              bf[nt][gr][h] =
+                  half2_bits(on[nt][2 * h] ? p[nt][2 * h] * ratio_v[h][gr] : 0.f,
+                             on[nt][2 * h + 1] ? p[nt][2 * h + 1] * ratio_v[h][gr] : 0.f);
       }
-      uint32_t bf[NT][G][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float ref = m[nt][e & 1];
-          const float w = ex2(p[nt][e] - (ref == kNegInf ? 0.f : ref));
-          // a masked token's grid may be anything (NaN too): its weight is 0 by selection
-          const bool on = inner || p[nt][e] != kNegInf;
-          l[nt][e & 1] += on ? w * rs[e >> 1] : 0.f;
-          p[nt][e] = on ? w : 0.f;
-        }
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int gr = 0; gr < G; ++gr)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float w0 = p[nt][2 * h] == 0.f ? 0.f : p[nt][2 * h] * ratio_v[h][gr];
-            const float w1 = p[nt][2 * h + 1] == 0.f ? 0.f : p[nt][2 * h + 1] * ratio_v[h][gr];
-            bf[nt][gr][h] = transpose8x8(half2_bits(w0, w1));
-          }
-      }
+          for (int h = 0; h < 2; ++h) bf[nt][gr][h] = transpose8x8(bf[nt][gr][h]);
 
       // ---- o: 16 dims x 8 NT rows per product ----
 #pragma unroll
@@ -626,7 +687,10 @@ cache_attend_kernel(const Level a) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint8_t* z = zvp + (2 * t + 8 * h) * G + gr;
-          zp[h] = z[0] | static_cast<uint32_t>(z[G]) << 16;
+          if constexpr (G == 1)
+            zp[h] = __byte_perm(*reinterpret_cast<const uint16_t*>(z), 0, 0x4140);
+          else
+            zp[h] = z[0] | static_cast<uint32_t>(z[G]) << 16;
         }
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
@@ -649,16 +713,17 @@ cache_attend_kernel(const Level a) {
             od[h] = BITS == 4 ? (w[h][wi] >> 4) & 0x0F0F0F0Fu : w[h][wi];
           }
 #pragma unroll
-          for (int i = 0; i < kPairs; ++i) {
+          for (int i2 = 0; i2 < kPairs; ++i2) {
             uint32_t a0, a1, a2, a3;
             if constexpr (BITS == 4) {
-              const uint32_t sel = i | (8 | i) << 4 | (4 + i) << 8 | (8 | i) << 12;
+              const uint32_t sel = i2 | (8 | i2) << 4 | (4 + i2) << 8 | (8 | i2) << 12;
               a0 = prmt(ev[0], ev[1], sel);
               a1 = prmt(od[0], od[1], sel);
               a2 = prmt(ev[2], ev[3], sel);
               a3 = prmt(od[2], od[3], sel);
             } else {
-              const uint32_t s0 = (2 * i) | (4 + 2 * i) << 8, s1 = (2 * i + 1) | (5 + 2 * i) << 8;
+              const uint32_t s0 = (2 * i2) | (4 + 2 * i2) << 8;
+              const uint32_t s1 = (2 * i2 + 1) | (5 + 2 * i2) << 8;
               a0 = prmt(ev[0], ev[1], s0) & 0x00FF00FFu;
               a1 = prmt(od[0], od[1], s1) & 0x00FF00FFu;
               a2 = prmt(ev[2], ev[3], s0) & 0x00FF00FFu;
@@ -668,13 +733,14 @@ cache_attend_kernel(const Level a) {
             a1 = sub_f16x2(a1, zp[0]);
             a2 = sub_f16x2(a2, zp[1]);
             a3 = sub_f16x2(a3, zp[1]);
-            const int tile = gr * (GROUP / 16) + wi * kPairs + i;
+            const int tile = gr * (GROUP / 16) + wi * kPairs + i2;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               mma_f16(o[nt][tile], a0, a1, a2, a3, bf[nt][gr][0], bf[nt][gr][1]);
           }
         }
       }
+      st = st + C::kStage == ring + C::kRing ? ring : st + C::kStage;
       __syncwarp();          // every lane is done with the stage that the next copies overwrite
       issue(issued);
     }
@@ -716,7 +782,7 @@ cache_attend_kernel(const Level a) {
     const int64_t slot = tile0 == 0 ? 2 * me + 1 : 2 * me;
     for (int k = threadIdx.x; k < R * (D / 4); k += kThreads) {
       const int r = k / (D / 4), d = k % (D / 4) * 4;
-      const int64_t j = row_first + r;
+      const int j = row_first + r;
       if (j >= n_rows) continue;
       float top = kNegInf;
 #pragma unroll
@@ -740,8 +806,9 @@ cache_attend_kernel(const Level a) {
       acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       const float lse = den == 0.f ? kNegInf : (top == kNegInf ? 0.f : top) + log2f(den);
       if (whole) {
-        finish<D>(a, s.row0 + j / a.ratio, head * a.ratio + static_cast<int>(j % a.ratio), d, acc,
-                  lse);
+        const uint32_t tk = static_cast<uint32_t>(j) / static_cast<uint32_t>(a.ratio);
+        finish<D>(a, s.row0 + static_cast<int64_t>(tk),
+                  head * a.ratio + j - static_cast<int>(tk) * a.ratio, d, acc, lse);
       } else {
         *reinterpret_cast<float4*>(a.part + (slot * R + r) * D + d) = acc;
         if (d == 0) a.part_lse[slot * R + r] = lse;
@@ -749,17 +816,30 @@ cache_attend_kernel(const Level a) {
     }
     if (!whole && tile0 == 0 && threadIdx.x == 0) {
       // this run holds the item's beginning: runs me + 1 .. last hold the rest
-      const int64_t t_last = base + (item + 1) * s.tiles_per - 1;
+      const int64_t t_last = item0 + s.tiles_per - 1;
       int64_t last = me + 1;
       while (last + 1 < cut.parts && cut.begin(last + 1) <= t_last) ++last;
       int32_t* join = a.join + me * 8;
-      join[1] = static_cast<int32_t>(min(n_rows - row_first, static_cast<int64_t>(R)));
+      join[1] = min(n_rows - row_first, R);
       join[2] = head;
-      *reinterpret_cast<int64_t*>(join + 4) = s.row0;
-      *reinterpret_cast<int64_t*>(join + 6) = row_first;
+      join[4] = s.row0;
+      join[5] = row_first;
       join[0] = static_cast<int32_t>(last - me);
     }
+    // ---- the next item ----
     cur += run;
+    tile0 = 0;
+    item0 = cur;
+    if (++rt == s.row_tiles) {
+      rt = 0;
+      if (++head == a.cache.heads && cur < end) {
+        head = 0;
+        do {
+          if (b + 1 >= sequences) return;   // only if the lengths changed under this kernel
+          s = get_sequence<R>(a, ++b);
+        } while (s.tiles == 0);
+      }
+    }
   }
 }
 
@@ -779,8 +859,8 @@ cache_join_kernel(const Level a) {
   const int runs = __ldcg(join);
   if (runs == 0) return;
   const int live = __ldcg(join + 1), head = __ldcg(join + 2);
-  const int64_t row0 = __ldcg(reinterpret_cast<const long long*>(join + 4));
-  const int64_t row_first = __ldcg(reinterpret_cast<const long long*>(join + 6));
+  const int64_t row0 = __ldcg(join + 4);
+  const int row_first = __ldcg(join + 5);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows_here = R / gridDim.y;
   const int per_row = max(1, kJoinWarps / rows_here);     // warps of a row
@@ -850,9 +930,9 @@ cache_join_kernel(const Level a) {
       float x[4];
 #pragma unroll
       for (int k = 0; k < kVec; ++k) x[k] = acc[k] * inv;
-      const int64_t j = row_first + r;
+      const int j = row_first + r;
       const int64_t tok = row0 + j / a.ratio;
-      const int qhead = head * a.ratio + static_cast<int>(j % a.ratio);
+      const int qhead = head * a.ratio + j % a.ratio;
       if constexpr (kVec == 4) {
         finish<D>(a, tok, qhead, lane * 4, make_float4(x[0], x[1], x[2], x[3]), lse);
       } else {
@@ -922,7 +1002,8 @@ size_t cache_workspace_bytes(int heads, int dim, int64_t n, int ratio, bool shar
   size_t b = slots_bytes(dim);
   if (shared) {
     const size_t rows = static_cast<size_t>(n) * heads * ratio;
-    b += align_up(rows * 4, 256) + align_up(rows * dim * 4, 256);
+    b += align_up(rows * 4, 256) + align_up(rows * dim * 4, 256) +
+         prefix_workspace_bytes(heads, dim, n, ratio);
   }
   return b;
 }
@@ -960,6 +1041,13 @@ gptq_status run_cache_attend(const CacheView& c, const CacheRows& r, int dim, in
     const size_t rows = static_cast<size_t>(r.n) * c.heads * q.ratio;
     a.mid_lse = reinterpret_cast<float*>(w);
     a.mid = reinterpret_cast<float*>(w + align_up(rows * 4, 256));
+    if (r.n * q.ratio > 16) {
+      w += align_up(rows * 4, 256) + align_up(rows * dim * 4, 256);
+      a.out = nullptr;
+      const gptq_status st = level(a, (r.n * q.ratio + r.batch - 1) / r.batch);
+      if (st != GPTQ_OK) return st;
+      return run_cache_prefix(c, r, dim, bits, group, q, a.mid, a.mid_lse, w, info, stream);
+    }
     Level p = a;
     p.out = nullptr;
     p.fixed_len = q.prefix_len;

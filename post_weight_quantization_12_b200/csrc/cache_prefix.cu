@@ -1,0 +1,942 @@
+// Attention of many rows over one common sequence of the quantized cache, on the tcgen05 tensor
+// cores: the shared prefix of a batch.
+//
+// All query rows of a cache head (tokens x query heads of it) meet the same keys, so the codes are
+// unpacked once per 256 rows, into fp16 images that stay in shared memory:
+//   S = Q K^T     128 rows x 128 tokens, Q and the image of K both K-major
+//   P = 2^(S - m) fp16, written over S in tensor memory, where the second product reads it
+//   O += P V      128 rows x D, the image of V with the dimensions contiguous (MN-major)
+// The image of a value is s' (q - z), q - z exact and one rounding to fp16 (2^-12), s' = s 2^(T - E)
+// with E the largest exponent among the tile's scales, so that the largest image stays below 65504:
+// values 2^-36 of the tile's largest are lost, whatever the scales are. The power of two goes back
+// in fp32: into the factor of S (K), into O's reference exponent (V, a running maximum).
+// m follows the running maximum of a row lazily: while S stays below m + 8 it is kept (weights up
+// to 2^8 fit in fp16), so O is rescaled in tensor memory only a few times.
+//
+// A CTA (one per SM) holds two row tiles of 128 and goes over a run of 128-token tiles:
+//   warps 0-3, 4-7   softmax of row tile 0 and 1, one thread a row; they also bring Q in and write
+//                    the results
+//   warps 8-15       unpack K and V of the next tiles into two buffers each, loads a tile ahead
+//   warp 16          issues the products: PV(0), QK(0) of the next tile, PV(1), QK(1), so one
+//                    tile's softmax runs under the other's products
+// With no more than 128 rows in an item, both softmax groups take the same rows and every other
+// token tile. The runs' results (row, fp32, with its log-sum) are joined by cache_merge_kernel.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "cache.cuh"
+
+namespace gptq {
+namespace {
+
+constexpr int kTok = 128;                  // tokens of a tile
+constexpr int kDq0 = 8, kDqWarps = 8;      // the unpacking warps
+constexpr int kDqRows = kTok / kDqWarps;   // rows of a tile that one of them takes
+constexpr int kMmaWarp = kDq0 + kDqWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr float kNegInf = -INFINITY;
+
+struct Prefix {
+  CacheView cache;
+  const int32_t* table;
+  int64_t len;
+  const __nv_bfloat16* q;
+  int64_t ldq, n;
+  int ratio;
+  float scale_log2;
+  int row_items;                // items of up to 256 rows of a head
+  int tiles, splits;
+  int units;                    // heads * row_items * splits
+  float* part;                  // [units][2][128][D]
+  float* part_lse;              // [units][2][128]
+  int32_t* info;
+};
+
+template <int D, int BITS>
+struct Smem {
+  static constexpr int kTileBytes = kTok * D * 2;         // an operand tile: D / 64 halves of 16 KB
+  static constexpr int kCodeBytes = kTok * D * BITS / 8;  // a tile's codes of K or V
+  static constexpr int kAhead = BITS == 4 ? 2 : 1;        // steps whose codes are on the way
+  // Q 0, Q 1, K 0, K 1, V 0, V 1, codes
+  static constexpr int kBytes = 6 * kTileBytes + kAhead * 2 * kCodeBytes + 1024;
+};
+
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};"
+               ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7]), "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// One lane of a converged warp, the same at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// Waits for the tensor-memory loads issued so far; the registers are named so that nothing that
+// uses them moves ahead of the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float pow2(int e) {          // e in [-126, 127]
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// One unit of work: an item (a cache head and up to 256 of its rows) and a run of token tiles.
+struct Unit {
+  int head, tile0, steps;       // steps: token tiles
+  int row0, rows;               // rows of the item
+  bool two;                     // two row tiles; else both softmax groups share one
+};
+__device__ __forceinline__ Unit get_unit(const Prefix& a, int u) {
+  Unit w;
+  const uint32_t item = static_cast<uint32_t>(u) / static_cast<uint32_t>(a.splits);
+  const uint32_t split = static_cast<uint32_t>(u) - item * a.splits;
+  w.head = static_cast<int>(item / static_cast<uint32_t>(a.row_items));
+  w.row0 = static_cast<int>(item - w.head * static_cast<uint32_t>(a.row_items)) * 256;
+  w.rows = min(static_cast<int>(a.n) * a.ratio - w.row0, 256);
+  w.two = w.rows > 128;
+  // tiles <= 2^23 and splits <= 2 SMs: the products fit in 32 bits
+  const uint32_t tiles = static_cast<uint32_t>(a.tiles), splits = static_cast<uint32_t>(a.splits);
+  w.tile0 = static_cast<int>(tiles * split / splits);
+  w.steps = static_cast<int>(tiles * (split + 1) / splits) - w.tile0;
+  return w;
+}
+// The r-th step of softmax group i, and how many it has.
+__device__ __forceinline__ int step_of(const Unit& w, int i, int r) { return w.two ? r : 2 * r + i; }
+__device__ __forceinline__ int steps_of(const Unit& w, int i) {
+  return w.two ? w.steps : (w.steps + 1 - i) / 2;
+}
+
+template <int D, int BITS, int GROUP>
+__global__ void __launch_bounds__(kThreads, 1)
+cache_prefix_kernel(const Prefix a) {
+  constexpr int G = D / GROUP, RB = D * BITS / 8;
+  using SM = Smem<D, BITS>;
+  constexpr int kTile = SM::kTileBytes;
+  constexpr int kTop = BITS == 4 ? 11 : 7;       // images below 2^(kTop + 1) (2^BITS - 1) < 65504
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_align<1024>(smem_raw);
+  auto q_tile = [&](int i) { return smem + i * kTile; };
+  auto k_tile = [&](int b) { return smem + (2 + b) * kTile; };
+  auto v_tile = [&](int b) { return smem + (4 + b) * kTile; };
+  auto code_slot = [&](int b, int h) { return smem + 6 * kTile + (2 * b + h) * SM::kCodeBytes; };
+  __shared__ __align__(8) uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], mma_done;
+  __shared__ __align__(16) uint32_t valid[4][4];   // of step s in slot s % 4: tokens that count
+  __shared__ int k_exp[4], v_exp[4];               // ... and the exponents of its images
+  __shared__ uint32_t warp_top[2][kDqWarps][2];
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ volatile int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&q_full[b], 128);
+      mbar_init(&k_full[b], 32 * kDqWarps);
+      mbar_init(&k_empty[b], 1);
+      mbar_init(&v_full[b], 32 * kDqWarps);
+      mbar_init(&v_empty[b], 1);
+      mbar_init(&s_full[b], 1);
+      mbar_init(&p_full[b], 128);
+      mbar_init(&pv_done[b], 1);
+    }
+    mbar_init(&mma_done, 1);
+    abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&tmem_base_sh, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  auto tm_s = [&](int i) { return tmem + 128 * i; };             // S, and P over its first half
+  auto tm_o = [&](int i) { return tmem + 256 + D * i; };
+  griddep_wait();
+  griddep_launch_dependents();
+  int32_t* info = a.info;
+
+  if (warp < kDq0) {
+    // ---- softmax group i, one row a thread ----
+    const int i = warp >> 2;
+    const int r = threadIdx.x & 127;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    uint32_t c_step = 0;        // steps of this group so far
+    uint32_t g_base = 0;         // steps of the units before
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+      const Unit w = get_unit(a, u);
+      const int row = w.two ? i * 128 + r : r;       // of the item
+      const bool live = row < w.rows;
+      const int my_steps = steps_of(w, i);
+      // Q: fp16 after a power of two per row (group 1 writes its own tile only)
+      float row_c = 0.f;
+      {
+        uint4 raw[D / 8];
+        float top = 0.f;
+        if (live) {
+          const int j = w.row0 + row;
+          const int tok = static_cast<int>(static_cast<uint32_t>(j) / static_cast<uint32_t>(a.ratio));
+          const uint4* src = reinterpret_cast<const uint4*>(
+              a.q + tok * a.ldq +
+              (static_cast<int64_t>(w.head) * a.ratio + (j - tok * a.ratio)) * D);
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) raw[c] = __ldg(src + c);
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[k] << 16)),
+                                     fabsf(__uint_as_float(x[k] & 0xFFFF0000u))));
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) raw[c] = make_uint4(0, 0, 0, 0);
+        }
+        const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
+        // a negative scale goes into Q, so the largest score is the largest product
+        const float up = (e > 127 ? 1.f : pow2(14 - e)) * (a.scale_log2 < 0.f ? -1.f : 1.f);
+        row_c = (e > 127 ? 1.f : pow2(e - 14)) * fabsf(a.scale_log2);
+        if (w.two || i == 0) {
+          uint8_t* dst = q_tile(i) + r * 128;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              f[2 * k] = __uint_as_float(x[k] << 16) * up;
+              f[2 * k + 1] = __uint_as_float(x[k] & 0xFFFF0000u) * up;
+            }
+            // in the order that 4-bit codes come out of their word
+            const uint4 h = BITS == 4 ? make_uint4(half2_bits(f[0], f[4]), half2_bits(f[1], f[5]),
+                                                   half2_bits(f[2], f[6]), half2_bits(f[3], f[7]))
+                                      : make_uint4(half2_bits(f[0], f[1]), half2_bits(f[2], f[3]),
+                                                   half2_bits(f[4], f[5]), half2_bits(f[6], f[7]));
+            *reinterpret_cast<uint4*>(dst + (c >> 3) * (kTok * 128) +
+                                      (((c & 7) ^ (r & 7)) << 4)) = h;
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&q_full[i]);
+        }
+      }
+      float m = kNegInf, l = 0.f;
+      int e_ref = -1000;
+      for (int k = 0; k < my_steps; ++k, ++c_step) {
+        const uint32_t gs = g_base + step_of(w, i, k);
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[i], c_step & 1, &abort_flag, info));
+        if (!ok) break;
+        tc_fence_after();
+        const int slot = gs & 3;
+        const int e_new = v_exp[slot];
+        const float xs = row_c * pow2(k_exp[slot]);
+        const uint32_t ts = tm_s(i) + lane_base;
+        uint32_t va[16], vb[16];
+        const uint4 vm = *reinterpret_cast<const uint4*>(valid[slot]);
+        if ((vm.x & vm.y & vm.z & vm.w) != 0xFFFFFFFFu) {
+          // tokens that do not count: their products become -inf
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            const uint32_t mask = valid[slot][c >> 1] >> (16 * (c & 1));
+            tmem_ld_32x32b_x16(ts + 16 * c, va);
+            tmem_wait_ld(va);
+#pragma unroll
+            for (int t = 0; t < 16; ++t)
+              if (!(mask >> t & 1u)) va[t] = __float_as_uint(kNegInf);
+            tmem_st_32x32b_x16(ts + 16 * c, va);
+          }
+          tmem_wait_st();
+        }
+        // largest product of the row; each load runs under the maxima of the one before
+        float top = kNegInf;
+        auto max16 = [&](const uint32_t (&v)[16]) {
+          float x = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
+          float y = fmaxf(__uint_as_float(v[2]), __uint_as_float(v[3]));
+#pragma unroll
+          for (int t = 4; t < 16; t += 4) {
+            x = fmaxf(fmaxf(x, __uint_as_float(v[t])), __uint_as_float(v[t + 1]));
+            y = fmaxf(fmaxf(y, __uint_as_float(v[t + 2])), __uint_as_float(v[t + 3]));
+          }
+          top = fmaxf(top, fmaxf(x, y));
+        };
+        tmem_ld_32x32b_x16(ts, va);
+#pragma unroll
+        for (int c = 0; c < 8; c += 2) {
+          tmem_wait_ld(va);
+          tmem_ld_32x32b_x16(ts + 16 * c + 16, vb);
+          max16(va);
+          tmem_wait_ld(vb);
+          if (c < 6) tmem_ld_32x32b_x16(ts + 16 * c + 32, va);
+          max16(vb);
+        }
+        top = top == kNegInf ? kNegInf : top * xs;
+        const bool grow = top > m + 8.f || (m == kNegInf && top > kNegInf);
+        if (__any_sync(0xffffffffu, grow) || e_new > e_ref) {
+          const float m_new = fmaxf(m, top);
+          const float f = m == kNegInf ? 0.f : ex2(m - m_new);
+          l *= f;
+          m = m_new;
+          if (k > 0) {
+            // O of the steps so far: the products that made it are complete (they were issued
+            // before this step's S)
+            const float fo = f * (e_ref < e_new - 120 ? 0.f : pow2(e_ref - e_new));
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              tmem_ld_32x32b_x16(tm_o(i) + lane_base + 16 * c, va);
+              tmem_wait_ld(va);
+#pragma unroll
+              for (int t = 0; t < 16; ++t) va[t] = __float_as_uint(__uint_as_float(va[t]) * fo);
+              tmem_st_32x32b_x16(tm_o(i) + lane_base + 16 * c, va);
+            }
+          }
+          e_ref = e_new;
+        }
+        // weights, written over the S that they come from (chunk c of 16 over columns 8 c ..,
+        // which have been read by then)
+        const float ref = m == kNegInf ? 0.f : m;
+        const float2 xs2 = make_float2(xs, xs), ref2 = make_float2(-ref, -ref);
+        float2 sum = make_float2(0.f, 0.f), sum_b = sum;
+        auto weigh = [&](const uint32_t (&v)[16], int c) {
+          uint32_t p[8];
+#pragma unroll
+          for (int t = 0; t < 16; t += 2) {
+            const float2 x =
+                fma2(make_float2(__uint_as_float(v[t]), __uint_as_float(v[t + 1])), xs2, ref2);
+            const float2 w = make_float2(ex2(x.x), ex2(x.y));
+            if (t & 2) sum = add2(sum, w); else sum_b = add2(sum_b, w);
+            p[t / 2] = half2_bits(w.x, w.y);
+          }
+          tmem_st_32x32b_x8(ts + 8 * c, p);
+        };
+        tmem_ld_32x32b_x16(ts, va);
+#pragma unroll
+        for (int c = 0; c < 8; c += 2) {
+          tmem_wait_ld(va);
+          tmem_ld_32x32b_x16(ts + 16 * c + 16, vb);
+          weigh(va, c);
+          tmem_wait_ld(vb);
+          if (c < 6) tmem_ld_32x32b_x16(ts + 16 * c + 32, va);
+          weigh(vb, c + 1);
+        }
+        sum = add2(sum, sum_b);
+        l += sum.x + sum.y;
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&p_full[i]);
+      }
+      g_base += w.steps;
+      if (!ok) break;
+      // the row's result
+      const int64_t slot = 2 * static_cast<int64_t>(u) + i;
+      float lse = kNegInf;
+      if (my_steps > 0) {
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_bounded(&pv_done[i], (c_step - 1) & 1, &abort_flag, info));
+        if (!ok) break;
+        tc_fence_after();
+        lse = l == 0.f ? kNegInf : (m == kNegInf ? 0.f : m) + log2f(l);
+        const float f = l == 0.f ? 0.f : 1.f / l;
+        // 2^e_ref in two factors: each within fp32's normal range
+        const float f0 = pow2(e_ref / 2), f1 = pow2(e_ref - e_ref / 2);
+        float* dst = a.part + (slot * 128 + r) * D;
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(tm_o(i) + lane_base + 16 * c, v);
+          tmem_wait_ld(v);
+#pragma unroll
+          for (int t = 0; t < 16; ++t)
+            v[t] = __float_as_uint(__uint_as_float(v[t]) * f * f0 * f1);
+          if (live) {
+#pragma unroll
+            for (int t = 0; t < 16; t += 8) {
+              uint4 lo, hi;
+              if constexpr (BITS == 4) {      // columns hold dims 0 4 1 5 2 6 3 7 of each eight
+                lo = make_uint4(v[t], v[t + 2], v[t + 4], v[t + 6]);
+                hi = make_uint4(v[t + 1], v[t + 3], v[t + 5], v[t + 7]);
+              } else {
+                lo = make_uint4(v[t], v[t + 1], v[t + 2], v[t + 3]);
+                hi = make_uint4(v[t + 4], v[t + 5], v[t + 6], v[t + 7]);
+              }
+              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                           ::"l"(dst + 16 * c + t), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w),
+                             "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
+            }
+          }
+        }
+        tc_fence_before();
+      }
+      if (live) a.part_lse[slot * 128 + r] = lse;
+    }
+  } else if (warp < kMmaWarp) {
+    // ---- unpack: lane t of a row takes 32 dims (8-bit codes: two pieces of 16, half a row apart,
+    // so that the lanes of a load meet whole sectors); a warp takes 16 rows of the tile ----
+    constexpr int LPR = D / 32, RPI = 32 / LPR;                // lanes a row, rows an access
+    constexpr int KI = kDqRows / RPI;
+    constexpr int kVec = BITS == 4 ? 1 : 2;                    // 16-byte loads of a lane's codes
+    const int dw = warp - kDq0, t = lane % LPR, g = lane / LPR;
+    // first dim of piece v of this lane
+    auto dim_of = [&](int v) { return BITS == 4 ? 32 * t : 16 * t + v * (D / 2); };
+    constexpr int kS = (G + 1) / 2;      // words of a row's scales
+    // The steps, unit by unit. Three things run ahead of the unpacking, so that none waits for
+    // another's loads: the page lookup of step gs + kAhead + 1, the codes of step gs + kAhead and
+    // the grids of step gs + 1.
+    struct At {
+      int u, left, tile, head;       // left: steps to come in this unit
+    };
+    auto enter = [&](At& x, int u) {
+      x.u = u;
+      if (u < a.units) {
+        const Unit w = get_unit(a, u);
+        x.left = w.steps;
+        x.tile = w.tile0;
+        x.head = w.head;
+      }
+    };
+    auto next = [&](At& x) {
+      if (x.u >= a.units) return;
+      ++x.tile;
+      if (--x.left == 0) enter(x, x.u + gridDim.x);
+    };
+    // page table entry of the warp's row `lane % 16` of a step, -1 past the end; and from it the row's
+    // number in the cache, -1 if the token does not count
+    int32_t entry = -1, entry_off = 0, entry_head = 0;
+    bool entry_in = false;
+    auto look = [&](const At& x) {
+      const int pos = x.tile * kTok + dw * kDqRows + lane % kDqRows;   // prefix_len <= 2^30
+      entry_in = x.u < a.units && pos < static_cast<int>(a.len);
+      entry = entry_in ? __ldg(a.table + (pos >> a.cache.page_shift)) : -1;
+      entry_off = pos & ((1 << a.cache.page_shift) - 1);
+      entry_head = x.head;
+    };
+    auto resolve = [&]() -> int64_t {
+      if (entry >= 0 && entry < a.cache.pages)
+        return cache_row(a.cache, entry, entry_head, entry_off);
+      if (entry_in) record_info(info, GPTQ_INFO_BAD_PAGE);
+      return -1;
+    };
+    // codes on their way to the slots: each lane copies what it will unpack
+    auto copy_codes = [&](int64_t row, int b, int h) {
+      uint8_t* dst = code_slot(b, h) + dw * (SM::kCodeBytes / kDqWarps) + lane * 16;
+      const uint8_t* base = a.cache.half[h].codes + 16 * t;
+      const int64_t from = max(row, static_cast<int64_t>(0));
+#pragma unroll
+      for (int k = 0; k < KI; ++k) {
+        const uint8_t* src = base + __shfl_sync(0xffffffffu, from, k * RPI + g) * RB;
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) cp_async16(dst + (k * kVec + v) * 512, src + v * (RB / 2));
+      }
+      cp_commit();
+    };
+    // scales (bf16 pairs) and zeros (bytes) of the warp's row `lane % 16` of K and V
+    uint32_t sc[2][kS], zr[2];
+    auto load_grids = [&](int64_t row) {
+      const int64_t from = max(row, static_cast<int64_t>(0)) * G;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint16_t* s = a.cache.half[h].scales + from;
+        const uint8_t* z = a.cache.half[h].zeros + from;
+        if constexpr (G == 1) {
+          sc[h][0] = __ldg(s);
+          zr[h] = __ldg(z);
+        } else if constexpr (G == 2) {
+          sc[h][0] = __ldg(reinterpret_cast<const uint32_t*>(s));
+          zr[h] = __ldg(reinterpret_cast<const uint16_t*>(z));
+        } else {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(s));
+          sc[h][0] = v.x;
+          sc[h][kS - 1] = v.y;
+          zr[h] = __ldg(reinterpret_cast<const uint32_t*>(z));
+        }
+      }
+    };
+    bool ok = true;
+    uint32_t gs = 0;
+    At now;
+    enter(now, blockIdx.x);
+    At ahead = now;              // the step whose page is looked up next
+    int64_t rows[SM::kAhead + 1];    // of steps gs, gs + 1, ..
+#pragma unroll
+    for (int k = 0; k < SM::kAhead; ++k) {
+      look(ahead);
+      next(ahead);
+      rows[k] = resolve();
+      copy_codes(rows[k], k, 0);
+      copy_codes(rows[k], k, 1);
+    }
+    look(ahead);
+    next(ahead);
+    load_grids(rows[0]);
+    int v_ref = -1000, v_unit = -1;
+    for (; now.u < a.units; ++gs) {
+      const int b = gs & 1, slot = gs & 3;
+      const int cb = SM::kAhead == 1 ? 0 : b;
+      const uint32_t ph = (gs >> 1) & 1u;
+      if (now.u != v_unit) v_ref = -1000;
+      v_unit = now.u;
+      const bool counts = rows[0] >= 0;
+      // a token that does not count: zero scales, so its images are zeros
+      if (!counts) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int k = 0; k < kS; ++k) sc[h][k] = 0;
+      }
+      // the tile's largest scales (as bits; not the ones that are not finite)
+      uint32_t top[2] = {0, 0};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+          const uint32_t x = k & 1 ? sc[h][k / 2] >> 16 : sc[h][k / 2] & 0xFFFFu;
+          top[h] = max(top[h], x < 0x7F80u ? x : 0u);
+        }
+        top[h] = __reduce_max_sync(0xffffffffu, top[h]);
+      }
+      if (lane == 0) {
+        warp_top[gs & 1][dw][0] = top[0];
+        warp_top[gs & 1][dw][1] = top[1];
+      }
+      // all the warps leave together if one of them gave up
+      if (named_barrier_or(1, 32 * kDqWarps, !ok)) break;
+#pragma unroll
+      for (int x = 0; x < kDqWarps; ++x) {
+        top[0] = max(top[0], warp_top[gs & 1][x][0]);
+        top[1] = max(top[1], warp_top[gs & 1][x][1]);
+      }
+      int e[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) e[h] = max(static_cast<int>(top[h] >> 7) - 127, -107);
+      v_ref = max(v_ref, e[1]);
+      e[1] = v_ref;
+      // this step's grids move on to make room for the next one's
+      uint32_t s_now[2][kS], z_now[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        z_now[h] = zr[h];
+#pragma unroll
+        for (int k = 0; k < kS; ++k) s_now[h][k] = sc[h][k];
+      }
+      const uint32_t counting = __ballot_sync(0xffffffffu, counts);
+      next(now);
+      rows[SM::kAhead] = resolve();
+      look(ahead);
+      next(ahead);
+      load_grids(rows[1]);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        cp_wait<2 * SM::kAhead - 1>();
+        __syncwarp();
+        if (ok) ok = mbar_wait_bounded(h == 0 ? &k_empty[b] : &v_empty[b], ph ^ 1u, &abort_flag,
+                                       info);
+        if (h == 0) {
+          // slot s % 4 was last read by step s - 4's softmax, which PV(s - 4) followed
+          if (lane == 0)
+            reinterpret_cast<uint16_t*>(valid[slot])[dw] = static_cast<uint16_t>(counting);
+          if (threadIdx.x == 32 * kDq0) {
+            k_exp[slot] = e[0] - kTop;
+            v_exp[slot] = e[1] - kTop;
+          }
+        }
+        const float unit = pow2(max(kTop - (h == 0 ? e[0] : e[1]), -126));
+        const uint8_t* src = code_slot(cb, h) + dw * (SM::kCodeBytes / kDqWarps) + lane * 16;
+        uint8_t* tile = h == 0 ? k_tile(b) : v_tile(b);
+        uint32_t s_h[kS];
+#pragma unroll
+        for (int k = 0; k < kS; ++k) s_h[k] = h == 0 ? s_now[0][k] : s_now[1][k];
+        const uint32_t z_h = h == 0 ? z_now[0] : z_now[1];
+#pragma unroll
+        for (int k = 0; k < KI; ++k) {
+          const int rl = k * RPI + g, row = dw * kDqRows + rl;
+          uint32_t sw[kS];
+#pragma unroll
+          for (int x = 0; x < kS; ++x) sw[x] = __shfl_sync(0xffffffffu, s_h[x], rl);
+          const uint32_t zw = __shfl_sync(0xffffffffu, z_h, rl);
+#pragma unroll
+          for (int v = 0; v < kVec; ++v) {
+            const int group = dim_of(v) / GROUP;
+            const uint32_t s_w = kS == 2 && (group & 2) ? sw[kS - 1] : sw[0];
+            const uint32_t z = zw >> (8 * group) & 0xFFu;
+            const float f = __uint_as_float(group & 1 ? s_w & 0xFFFF0000u : s_w << 16) * unit;
+            const uint32_t s2 = half2_bits(f, f);
+            const uint32_t z2 = (0x6400u + z) * 0x00010001u;            // 1024 + z, exact
+            const uint4 w4 = *reinterpret_cast<const uint4*>(src + (k * kVec + v) * 512);
+            uint32_t wd[4] = {w4.x, w4.y, w4.z, w4.w};
+            // this piece's image: chunks of eight dims from chunk c0 of its 64-dim half
+            uint8_t* dst = tile + (dim_of(v) >> 6) * (kTok * 128) + row * 128;
+            const uint32_t c0 = (dim_of(v) & 63) >> 3;
+            if constexpr (BITS == 4) {
+              // lanes t and t + 2 store to different halves, of the same banks: they take their
+              // four chunks in another order, so the eight lanes of a store meet all the banks
+              const uint32_t flip = D == 128 ? (t & 2) : 0;
+              if (D == 128 && flip) {
+                uint32_t x = wd[0]; wd[0] = wd[2]; wd[2] = x;
+                x = wd[1]; wd[1] = wd[3]; wd[3] = x;
+              }
+              const uint32_t s16 = mul2(s2, 0x2C002C00u);               // s / 16
+              const uint32_t z16 = (0x6400u + 16 * z) * 0x00010001u;    // 1024 + 16 z
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t x = wd[c], x8 = x >> 8;
+                const uint4 y = make_uint4(
+                    mul2(sub2((x & 0x000F000Fu) | 0x64006400u, z2), s2),       // codes 0, 4
+                    mul2(sub2((x & 0x00F000F0u) | 0x64006400u, z16), s16),     // 1, 5, times 16
+                    mul2(sub2((x8 & 0x000F000Fu) | 0x64006400u, z2), s2),      // 2, 6
+                    mul2(sub2((x8 & 0x00F000F0u) | 0x64006400u, z16), s16));   // 3, 7
+                *reinterpret_cast<uint4*>(dst + (((c0 + (c ^ flip)) ^ (row & 7)) << 4)) = y;
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                uint32_t y[4] = {__byte_perm(wd[2 * c], 0x64646464u, 0x4140),
+                                 __byte_perm(wd[2 * c], 0x64646464u, 0x4342),
+                                 __byte_perm(wd[2 * c + 1], 0x64646464u, 0x4140),
+                                 __byte_perm(wd[2 * c + 1], 0x64646464u, 0x4342)};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) y[x] = mul2(sub2(y[x], z2), s2);
+                *reinterpret_cast<uint4*>(dst + (((c0 + c) ^ (row & 7)) << 4)) =
+                    make_uint4(y[0], y[1], y[2], y[3]);
+              }
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(h == 0 ? &k_full[b] : &v_full[b]);
+        // the slot is free (its lane has read it): the codes of a step to come
+        copy_codes(rows[SM::kAhead], cb, h);
+      }
+#pragma unroll
+      for (int k = 0; k < SM::kAhead; ++k) rows[k] = rows[k + 1];
+    }
+    cp_wait<0>();
+  } else {
+    // ---- products: the whole warp runs the loop, so that descriptors stay in uniform registers;
+    // one lane issues ----
+    constexpr uint32_t id_qk = make_idesc(/*f16*/ 0, 0, 0, 128, kTok);
+    constexpr uint32_t id_pv = make_idesc(/*f16*/ 0, 0, /*B MN-major*/ 1, 128, D);
+    const bool elected = elect_one();
+    // operand tiles are 1024-byte aligned: an offset in 16-byte units adds to a descriptor
+    const uint64_t q_desc = smem_desc(smem_u32(q_tile(0)), 16, 1024, kSwizzle128B);
+    const uint64_t k_desc = smem_desc(smem_u32(k_tile(0)), 16, 1024, kSwizzle128B);
+    const uint64_t v_desc = smem_desc(smem_u32(v_tile(0)), kTok * 128, 1024, kSwizzle128B);
+    uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_pv[2] = {0, 0};
+    uint32_t g_base = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, &abort_flag, info));
+      return ok;
+    };
+    for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+      const Unit w = get_unit(a, u);
+      auto qk = [&](int i, int s) {
+        const uint32_t gs = g_base + s;
+        const int b = gs & 1;
+        if (!wait(&k_full[b], (gs >> 1) & 1u)) return;
+        tc_fence_after();
+        if (elected) {
+          const uint64_t qd = q_desc + (w.two && i ? kTile / 16 : 0), kd = k_desc + b * (kTile / 16);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t at = ((kk >> 2) * (kTok * 128) + (kk & 3) * 32) / 16;
+            tc_mma_f16(tm_s(i), qd + at, kd + at, id_qk, kk ? 1u : 0u);
+          }
+          tc_commit(&s_full[i]);
+          if (!w.two || i == 1) tc_commit(&k_empty[b]);
+        }
+        __syncwarp();
+      };
+      if (!wait(&q_full[0], n_q[0] & 1)) break;
+      ++n_q[0];
+      if (w.two) {
+        if (!wait(&q_full[1], n_q[1] & 1)) break;
+        ++n_q[1];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (steps_of(w, i) == 0) continue;
+        // S takes the place of the last unit's weights
+        if (n_pv[i] > 0 && !wait(&pv_done[i], (n_pv[i] - 1) & 1)) break;
+        qk(i, step_of(w, i, 0));
+      }
+      const int most = steps_of(w, 0);
+      for (int r = 0; r < most && ok; ++r) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (!ok || r >= steps_of(w, i)) continue;
+          const uint32_t gs = g_base + step_of(w, i, r);
+          const int b = gs & 1;
+          if (!wait(&p_full[i], n_p[i] & 1)) break;
+          ++n_p[i];
+          if (!wait(&v_full[b], (gs >> 1) & 1u)) break;
+          tc_fence_after();
+          if (elected) {
+            const uint64_t vd = v_desc + b * (kTile / 16);
+#pragma unroll
+            for (int kk = 0; kk < kTok / 16; ++kk)
+              tc_mma_f16_ts(tm_o(i), tm_s(i) + kk * 8, vd + kk * (2048 / 16), id_pv,
+                            (r | kk) ? 1u : 0u);
+            tc_commit(&pv_done[i]);
+            if (!w.two || i == 1) tc_commit(&v_empty[b]);
+          }
+          __syncwarp();
+          ++n_pv[i];
+          if (r + 1 < steps_of(w, i)) {
+            // the next S takes the place of the weights that this product reads
+            if (!wait(&pv_done[i], (n_pv[i] - 1) & 1)) break;
+            qk(i, step_of(w, i, r + 1));
+          }
+        }
+      }
+      g_base += w.steps;
+    }
+    if (elected) {
+      tc_commit(&mma_done);           // let what was issued finish, after an error too
+      mbar_drain_bounded(&mma_done, 0);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// out = the results of the prefix's runs and, where a row met own positions, of its own level,
+// weighted by their sums. One warp a vector.
+struct Merge {
+  const float* part;
+  const float* part_lse;
+  const float* mid;             // own level: [n][heads ratio][D] and log-sums
+  const float* mid_lse;
+  __nv_bfloat16* out;
+  int64_t ldo, n, row_items, batch;
+  const int32_t* starts;
+  int heads, ratio, splits;
+};
+template <int D>
+__global__ void __launch_bounds__(256) cache_merge_kernel(const Merge a) {
+  constexpr int kVec = D / 32;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int per_row = a.heads * a.ratio;
+  // gridDim.y: blocks of eight vectors of a row
+  const int qh = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int64_t tok = blockIdx.x, v = tok * per_row + qh;
+  if (qh >= per_row) return;
+  const int64_t first = a.starts ? __ldg(a.starts) : 0;
+  const int64_t end = a.starts ? __ldg(a.starts + a.batch) : a.batch;
+  if (tok < first || tok >= end) return;       // not a row of any sequence: left as it is
+  const int head = qh / a.ratio;
+  const int64_t j = tok * a.ratio + (qh - head * a.ratio);
+  const int64_t ri = j >> 8;
+  int r = static_cast<int>(j & 255);
+  const bool two = a.n * a.ratio - ri * 256 > 128;
+  const int64_t u0 = (head * a.row_items + ri) * a.splits;
+  const int parts = two ? a.splits : 2 * a.splits;
+  const int wg = two ? r >> 7 : 0;
+  r &= 127;
+  float m = __ldcg(a.mid_lse + v), l = 0.f, acc[kVec];
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) acc[k] = 0.f;
+  if (m != kNegInf) {
+    l = 1.f;
+    const float* src = a.mid + v * D + lane * kVec;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) acc[k] = __ldcg(src + k);
+    if (!(m > kNegInf)) {        // NaN: keep it in the values, and a reference that compares
+      m = 0.f;
+      l = NAN;
+    }
+  }
+  constexpr int kAhead = 12;
+  for (int s0 = 0; s0 < parts; s0 += kAhead) {
+    float x[kAhead][kVec], lse[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      lse[k] = kNegInf;
+      if (s0 + k >= parts) continue;
+      const int64_t slot = two ? 2 * (u0 + s0 + k) + wg : 2 * u0 + s0 + k;
+      lse[k] = __ldcg(a.part_lse + slot * 128 + r);
+      const float* src = a.part + (slot * 128 + r) * D + lane * kVec;
+      if constexpr (kVec == 4)
+        *reinterpret_cast<float4*>(x[k]) = __ldcg(reinterpret_cast<const float4*>(src));
+      else
+        *reinterpret_cast<float2*>(x[k]) = __ldcg(reinterpret_cast<const float2*>(src));
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (lse[k] == kNegInf) continue;          // met nothing: its values were not written
+      const float top = fmaxf(m, lse[k]), ref = top == kNegInf ? 0.f : top;
+      const float f = m == kNegInf ? (l == 0.f ? 0.f : 1.f) : ex2(m - ref), w = ex2(lse[k] - ref);
+      m = top;
+      l = fmaf(l, f, w);
+#pragma unroll
+      for (int d = 0; d < kVec; ++d) acc[d] = fmaf(acc[d], f, w * x[k][d]);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t o[kVec / 2];
+#pragma unroll
+  for (int k = 0; k < kVec / 2; ++k) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+    o[k] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  __nv_bfloat16* dst = a.out + tok * a.ldo + static_cast<int64_t>(qh) * D + lane * kVec;
+  if constexpr (kVec == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+  else
+    *reinterpret_cast<uint32_t*>(dst) = o[0];
+}
+
+int64_t row_items_of(int64_t n, int ratio) { return (n * ratio + 255) / 256; }
+// Units never exceed this, so neither do the slots of a workspace.
+int64_t most_units(int64_t items) { return std::max<int64_t>(items, 2 * num_sms()); }
+
+}  // namespace
+
+size_t prefix_workspace_bytes(int heads, int dim, int64_t n, int ratio) {
+  const size_t slots = 2 * static_cast<size_t>(most_units(heads * row_items_of(n, ratio)));
+  return align_up(slots * 128 * 4, 256) + align_up(slots * 128 * dim * 4, 256);
+}
+
+gptq_status run_cache_prefix(const CacheView& c, const CacheRows& r, int dim, int bits, int group,
+                             const CacheQuery& q, const float* mid, const float* mid_lse, void* ws,
+                             int32_t* info, cudaStream_t stream) {
+  Prefix a{};
+  a.cache = c;
+  a.cache.width =
+      static_cast<int>((q.prefix_len + (static_cast<int64_t>(1) << c.page_shift) - 1) >> c.page_shift);
+  a.table = q.prefix_table;
+  a.len = q.prefix_len;
+  a.q = q.q;
+  a.ldq = q.ldq;
+  a.n = r.n;
+  a.ratio = q.ratio;
+  a.scale_log2 = q.scale * 1.4426950408889634f;
+  a.row_items = static_cast<int>(row_items_of(r.n, q.ratio));
+  a.tiles = static_cast<int>((q.prefix_len + kTok - 1) / kTok);
+  const int64_t items = static_cast<int64_t>(a.row_items) * c.heads;
+  // Runs per item: the fewest rounds of units times the length of one. A unit's start and end
+  // (queries in, results out) cost about as much as two tiles.
+  const int64_t sms = num_sms();
+  int64_t best = INT64_MAX;
+  const int64_t most = std::min<int64_t>(a.tiles, std::max<int64_t>(most_units(items) / items, 1));
+  a.splits = 1;
+  for (int64_t s = 1; s <= most; ++s) {
+    const int64_t cost = (items * s + sms - 1) / sms * ((a.tiles + s - 1) / s + 2);
+    if (cost < best) {
+      best = cost;
+      a.splits = static_cast<int>(s);
+    }
+  }
+  if (items * a.splits > INT32_MAX / 4) return GPTQ_EUNSUPPORTED;
+  a.units = static_cast<int>(items * a.splits);
+  const size_t slots = 2 * static_cast<size_t>(most_units(items));
+  a.part_lse = static_cast<float*>(ws);
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align_up(slots * 128 * 4, 256));
+  a.info = info;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.units, sms));
+  gptq_status st = dispatch_cache(dim, bits, group, [&](auto d, auto b, auto g) {
+    const auto kernel = cache_prefix_kernel<d.value, b.value, g.value>;
+    const gptq_status s =
+        set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), Smem<d.value, b.value>::kBytes);
+    return s != GPTQ_OK ? s
+                        : launch_pdl(kernel, dim3(grid), dim3(kThreads), Smem<d.value, b.value>::kBytes,
+                                     stream, a);
+  });
+  if (st != GPTQ_OK) return st;
+  Merge m{a.part, a.part_lse, mid, mid_lse, q.out, q.ldo, r.n, a.row_items, r.batch,
+          r.starts, c.heads, q.ratio, a.splits};
+  const dim3 mg(static_cast<unsigned>(r.n), static_cast<unsigned>((c.heads * q.ratio + 7) / 8));
+  return dim == 128 ? launch_pdl(cache_merge_kernel<128>, mg, dim3(256), 0, stream, m)
+                    : launch_pdl(cache_merge_kernel<64>, mg, dim3(256), 0, stream, m);
+}
+
+}  // namespace gptq
