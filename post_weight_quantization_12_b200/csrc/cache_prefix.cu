@@ -14,11 +14,12 @@
 // to 2^8 fit in fp16), so O is rescaled in tensor memory only a few times.
 //
 // A CTA (one per SM) holds two row tiles of 128 and goes over a run of 128-token tiles:
-//   warps 0-3, 4-7   softmax of row tile 0 and 1, one thread a row; they also bring Q in and write
+//   warp 0           issues the products: PV(0), QK(0) of the next tile, PV(1), QK(1), so one
+//                    tile's softmax runs under the other's products (the oldest warp: an SM's
+//                    scheduler lets it go first, and every other role waits for it)
+//   warps 4-7, 8-11  softmax of row tile 0 and 1, one thread a row; they also bring Q in and write
 //                    the results
-//   warps 8-15       unpack K and V of the next tiles into two buffers each, loads a tile ahead
-//   warp 16          issues the products: PV(0), QK(0) of the next tile, PV(1), QK(1), so one
-//                    tile's softmax runs under the other's products
+//   warps 12-15      unpack K and V of the next tiles into two buffers each, loads a tile ahead
 // With no more than 128 rows in an item, both softmax groups take the same rows and every other
 // token tile. The runs' results (row, fp32, with its log-sum) are joined by cache_merge_kernel.
 #include <cuda_runtime.h>
@@ -31,10 +32,12 @@ namespace gptq {
 namespace {
 
 constexpr int kTok = 128;                  // tokens of a tile
-constexpr int kDq0 = 8, kDqWarps = 8;      // the unpacking warps
-constexpr int kDqRows = kTok / kDqWarps;   // rows of a tile that one of them takes
-constexpr int kMmaWarp = kDq0 + kDqWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kSm0 = 4;                    // the first softmax warp
+constexpr int kDq0 = 12, kDqWarps = 4;      // the unpacking warps
+constexpr int kDqRows = kTok / kDqWarps;   // rows of a tile that one of them takes: one a lane
+static_assert(kDqRows == 32, "a lane a row");
+constexpr int kMmaWarp = 0;
+constexpr int kThreads = 32 * (kDq0 + kDqWarps);
 constexpr float kNegInf = -INFINITY;
 
 struct Prefix {
@@ -239,9 +242,9 @@ cache_prefix_kernel(const Prefix a) {
   griddep_launch_dependents();
   int32_t* info = a.info;
 
-  if (warp < kDq0) {
+  if (warp >= kSm0 && warp < kDq0) {
     // ---- softmax group i, one row a thread ----
-    const int i = warp >> 2;
+    const int i = (warp - kSm0) >> 2;
     const int r = threadIdx.x & 127;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     uint32_t c_step = 0;        // steps of this group so far
@@ -452,9 +455,9 @@ cache_prefix_kernel(const Prefix a) {
       }
       if (live) a.part_lse[slot * 128 + r] = lse;
     }
-  } else if (warp < kMmaWarp) {
+  } else if (warp >= kDq0) {
     // ---- unpack: lane t of a row takes 32 dims (8-bit codes: two pieces of 16, half a row apart,
-    // so that the lanes of a load meet whole sectors); a warp takes 16 rows of the tile ----
+    // so that the lanes of a load meet whole sectors); a warp takes 32 rows of the tile ----
     constexpr int LPR = D / 32, RPI = 32 / LPR;                // lanes a row, rows an access
     constexpr int KI = kDqRows / RPI;
     constexpr int kVec = BITS == 4 ? 1 : 2;                    // 16-byte loads of a lane's codes
@@ -482,12 +485,12 @@ cache_prefix_kernel(const Prefix a) {
       ++x.tile;
       if (--x.left == 0) enter(x, x.u + gridDim.x);
     };
-    // page table entry of the warp's row `lane % 16` of a step, -1 past the end; and from it the row's
+    // page table entry of the warp's row `lane` of a step, -1 past the end; and from it the row's
     // number in the cache, -1 if the token does not count
     int32_t entry = -1, entry_off = 0, entry_head = 0;
     bool entry_in = false;
     auto look = [&](const At& x) {
-      const int pos = x.tile * kTok + dw * kDqRows + lane % kDqRows;   // prefix_len <= 2^30
+      const int pos = x.tile * kTok + dw * kDqRows + lane;      // prefix_len <= 2^30
       entry_in = x.u < a.units && pos < static_cast<int>(a.len);
       entry = entry_in ? __ldg(a.table + (pos >> a.cache.page_shift)) : -1;
       entry_off = pos & ((1 << a.cache.page_shift) - 1);
@@ -512,7 +515,7 @@ cache_prefix_kernel(const Prefix a) {
       }
       cp_commit();
     };
-    // scales (bf16 pairs) and zeros (bytes) of the warp's row `lane % 16` of K and V
+    // scales (bf16 pairs) and zeros (bytes) of the warp's row `lane` of K and V
     uint32_t sc[2][kS], zr[2];
     auto load_grids = [&](int64_t row) {
       const int64_t from = max(row, static_cast<int64_t>(0)) * G;
@@ -615,8 +618,7 @@ cache_prefix_kernel(const Prefix a) {
                                        info);
         if (h == 0) {
           // slot s % 4 was last read by step s - 4's softmax, which PV(s - 4) followed
-          if (lane == 0)
-            reinterpret_cast<uint16_t*>(valid[slot])[dw] = static_cast<uint16_t>(counting);
+          if (lane == 0) valid[slot][dw] = counting;
           if (threadIdx.x == 32 * kDq0) {
             k_exp[slot] = e[0] - kTop;
             v_exp[slot] = e[1] - kTop;
@@ -693,7 +695,7 @@ cache_prefix_kernel(const Prefix a) {
       for (int k = 0; k < SM::kAhead; ++k) rows[k] = rows[k + 1];
     }
     cp_wait<0>();
-  } else {
+  } else if (warp == kMmaWarp) {
     // ---- products: the whole warp runs the loop, so that descriptors stay in uniform registers;
     // one lane issues ----
     constexpr uint32_t id_qk = make_idesc(/*f16*/ 0, 0, 0, 128, kTok);
