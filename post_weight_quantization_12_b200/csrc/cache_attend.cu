@@ -366,10 +366,10 @@ cache_attend_kernel(const Level a) {
   // scales and zeros of the 16 tokens: 6 G pieces of 16 bytes, a lane a piece
   const bool grid_lane = lane < 6 * G;
   const uint8_t* g_src;
-  int g_row;                    // bytes of a token
+  uint32_t g_row16;             // bytes of 16 tokens
   {
     const int half = lane >= 3 * G, e = lane - half * 3 * G;
-    g_row = e < 2 * G ? 2 * G : G;
+    g_row16 = e < 2 * G ? 32 * G : 16 * G;
     g_src = e < 2 * G ? reinterpret_cast<const uint8_t*>(a.cache.half[half].scales) + 16 * e
                       : a.cache.half[half].zeros + 16 * (e - 2 * G);
   }
@@ -405,7 +405,6 @@ cache_attend_kernel(const Level a) {
                        : -1;
     };
     int32_t pages_now = pages_from(0), pages_next = steps > 32 ? pages_from(32) : -1;
-    int32_t pages_old = -1;
 
     // the queries' loads go out while the pages come in
     constexpr int CPD = D / 4 / C::NPS;   // dims of a piece
@@ -425,31 +424,37 @@ cache_attend_kernel(const Level a) {
     }
 
     uint32_t put = ring_addr;             // the stage that is filled next
+    uint32_t haves = 0;                   // bit k: the k-th last step issued has a page
     auto issue = [&](int i) {
+      haves <<= 1;
       if (i < steps) {
         const int32_t page = __shfl_sync(0xffffffffu, pages_now, i & 31);
         if (page >= 0) {
-          const int off = (first + i * kTile) & ((1 << a.cache.page_shift) - 1);
-          const int64_t row = cache_row(a.cache, page, head, off);
-          const uint8_t* k0 = k_src + row * RB;
+          // rows / 16 of the cache stay below 2^31
+          const uint32_t off = (first + i * kTile) & ((1 << a.cache.page_shift) - 1);
+          const uint32_t row16 = ((static_cast<uint32_t>(page) * a.cache.heads + head)
+                                  << (a.cache.page_shift - 4)) + (off >> 4);
+          const uint8_t* k0 = k_src + static_cast<uint64_t>(row16) * (16 * RB);
+          const uint8_t* v0 = v_src + static_cast<uint64_t>(row16) * (16 * RB);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int p = 0; p < C::NPS; ++p)
               cp_async(put + lane * C::CPB + (h * C::NPS + p) * 32 * C::CPB,
                        k0 + 8 * h * RB + p * 4 * C::CPB, C::CPB);
-          const uint8_t* v0 = v_src + row * RB;
 #pragma unroll
           for (int h = 0; h < 4; ++h)
 #pragma unroll
             for (int gr = 0; gr < G; ++gr)
               cp_async(put + lane * C::VB + C::kK + (h * G + gr) * 32 * C::VB,
                        v0 + ((h & 1) + 8 * (h >> 1)) * RB + gr * (GROUP * BITS / 8), C::VB);
-          if (grid_lane) cp_async(put + C::kK + C::kV + 16 * lane, g_src + row * g_row, 16);
+          if (grid_lane)
+            cp_async(put + C::kK + C::kV + 16 * lane,
+                     g_src + static_cast<uint64_t>(row16) * g_row16, 16);
+          haves |= 1u;
         }
         put = put + C::kStage == ring_addr + C::kRing ? ring_addr : put + C::kStage;
         if ((i & 31) == 31) {      // the next step's page is in the next batch
-          pages_old = pages_now;
           pages_now = pages_next;
           pages_next = pages_from(i + 33);
         }
@@ -542,12 +547,11 @@ cache_attend_kernel(const Level a) {
     const uint8_t* st = ring;             // the stage that is consumed
     for (int i = 0; i < steps; ++i) {
       cp_wait<kStages - 2>();
+      // every lane's copies have landed, and every lane is done with the step before, whose stage
+      // the next copies fill
       __syncwarp();
-      // step i's page: its batch is the one being issued from, or the one before
-      const int issued = i + kStages - 1;      // the next step to issue
-      const bool in_old = (min(issued, steps) >> 5) != (i >> 5);
-      const bool have =
-          __shfl_sync(0xffffffffu, in_old ? pages_old : pages_now, i & 31) >= 0;
+      issue(i + kStages - 1);
+      const bool have = haves >> (kStages - 1) & 1u;
       const int pos = first + i * kTile;
 
       // grids of tokens g and g + 8
@@ -582,11 +586,12 @@ cache_attend_kernel(const Level a) {
         for (int e = 0; e < 4; ++e) x[nt][e] = 0.f;
 #pragma unroll
       for (int gr = 0; gr < G; ++gr) {
-        float c[NT][4];
+        // two chains of products, so that each waits half as long for the last
+        float c[NT][4], c2[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) c[nt][e] = 0.f;
+          for (int e = 0; e < 4; ++e) c[nt][e] = c2[nt][e] = 0.f;
 #pragma unroll
         for (int pp = 0; pp < C::NPS / G; ++pp) {
           const int p = gr * (C::NPS / G) + pp;
@@ -612,13 +617,13 @@ cache_attend_kernel(const Level a) {
                 const uint32_t u = hf ? wa[w] >> 8 : wa[w], v = hf ? wb[w] >> 8 : wb[w];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                  mma_f16(c[nt], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u,
+                  mma_f16(hf ? c2[nt] : c[nt], u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u,
                           v & 0x00F000F0u, qf[nt][4 * wi + 2 * hf], qf[nt][4 * wi + 2 * hf + 1]);
               }
             } else {
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma_f16(c[nt], __byte_perm(wa[w], 0, 0x4140), __byte_perm(wb[w], 0, 0x4140),
+                mma_f16(w & 1 ? c2[nt] : c[nt], __byte_perm(wa[w], 0, 0x4140), __byte_perm(wb[w], 0, 0x4140),
                         __byte_perm(wa[w], 0, 0x4342), __byte_perm(wb[w], 0, 0x4342),
                         qf[nt][2 * wi], qf[nt][2 * wi + 1]);
             }
@@ -628,8 +633,8 @@ cache_attend_kernel(const Level a) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            x[nt][e] = fmaf(sk[e >> 1][gr], fmaf(nz[e >> 1][gr], qsum[nt][gr][e & 1], c[nt][e]),
-                            x[nt][e]);
+            x[nt][e] = fmaf(sk[e >> 1][gr], fmaf(nz[e >> 1][gr], qsum[nt][gr][e & 1],
+                                                 c[nt][e] + c2[nt][e]), x[nt][e]);
       }
 
       // ---- weights relative to the running reference M ----
@@ -741,8 +746,6 @@ cache_attend_kernel(const Level a) {
         }
       }
       st = st + C::kStage == ring + C::kRing ? ring : st + C::kStage;
-      __syncwarp();          // every lane is done with the stage that the next copies overwrite
-      issue(issued);
     }
     cp_wait<0>();
 
