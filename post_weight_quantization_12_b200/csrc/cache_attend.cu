@@ -11,9 +11,10 @@
 // an fp16 word is that integer times 2^-24 exactly (a subnormal), so a mask (and for the odd codes
 // a byte permute) makes the operand. Zero points and scales are applied outside the products:
 //   q . k_t = s_t ((q . code_t) - z_t sum(q))             scale and zero of token t, per group
-// For o the zero points are subtracted from the operand itself (exact in fp16): a running sum of
-// codes, all positive, would lose 2^-24 of itself with each product, the tensor core's sums being
-// cut towards zero, and what is left after the zero points' share is a small part of it.
+// For o each step's products are followed by one whose rows all hold the step's zero points, so the
+// running sum stays one of s (code - z): a sum of codes, all positive, would lose 2^-24 of itself
+// with each product, the tensor core's sums being cut towards zero, and what is left after the zero
+// points' share is a small part of it.
 // The queries are fp16 after a power-of-two scale per row (bf16's 8 bits fit in fp16's 11; values
 // 2^-38 below the row's largest are lost). The weights w_t s_t become fp16 (rounding 2^-12 of each)
 // relative to their own running maximum: with u_t = x_t + log2(s_t) and M >= max u - 8 the operand
@@ -44,6 +45,18 @@ constexpr int kMaxResident = 4;             // CTAs per SM
 constexpr float kScaleFloor = 1.2621774e-29f;   // 2^-96, see below
 constexpr float kNegInf = -INFINITY;
 
+// A stage of the ring holds the codes of 16 tokens as they lie in the cache (K, then V, row after
+// row) and their grids. In shared memory the 16-byte chunks of a row are permuted: chunk c of row r
+// lies at c ^ swizzle(r). A product's row s is token slot_token(s). The two are chosen together so
+// that what the lanes of one load read (K: pieces of the rows of slots 0 .. 7; V: a piece of the
+// rows of slots 0, 2, 4, 6 or of the odd ones) meets different banks, for every row length and
+// group but one (V of 32-byte rows: two rows meet).
+__host__ __device__ constexpr int slot_token(int s) { return s ^ ((s >> 1) & 1); }
+template <int RB>
+__host__ __device__ constexpr int swizzle(int r) {
+  return ((r & 1) << 2 | (((r >> 1) ^ (r >> 2)) & 1) << 1 | ((r >> 2) & 1)) & (RB / 16 - 1);
+}
+
 template <int D, int BITS, int GROUP, int NT>
 struct Cfg {
   static constexpr int G = D / GROUP;
@@ -52,11 +65,11 @@ struct Cfg {
   static constexpr int NPS = NP < 1 ? 1 : NP;
   static constexpr int CPB = RB / 4 / NPS;                    // bytes of a K piece: 4, 8 or 16
   static constexpr int VGB = GROUP * BITS / 64;               // bytes of a lane's V share of a group
-  static constexpr int VB = VGB < 4 ? 4 : VGB;                // ... and what it fetches
-  static constexpr int kK = kStep * RB;                       // K bytes of a stage
-  static constexpr int kV = kStep * 8 * G * VB;               // V bytes of a stage
+  static constexpr int VB = VGB < 4 ? 4 : VGB;                // ... and what it reads
+  static constexpr int kK = kStep * RB;                       // K (or V) bytes of a stage
+  static constexpr int kCopies = kK / 512;                    // 16-byte copies of a lane for them
   static constexpr int kGridBytes = 96 * G;                   // scales and zeros of 16 tokens
-  static constexpr int kStage = kK + kV + kGridBytes;
+  static constexpr int kStage = 2 * kK + kGridBytes;
   static constexpr int kRing = kStages * kStage;
   static constexpr int R = 8 * NT;                            // rows of a row tile
   static constexpr int kPad = D + 4;
@@ -175,13 +188,12 @@ __device__ __forceinline__ Cut find_tile(const Level& a, int64_t part, Find& sh)
   return cut;
 }
 
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int bytes) {
-  if (bytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else if (bytes == 8)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+// Copies 16 bytes where `on` (a predicate of the instruction, not a branch).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+      "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst), "l"(src), "r"(on)
+      : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -208,11 +220,6 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
   return d;
 }
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -225,7 +232,7 @@ __device__ __forceinline__ float rcp(float x) {
 }
 __device__ __forceinline__ float lg2(float x) {
   float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
@@ -324,7 +331,9 @@ cache_attend_kernel(const Level a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Find find;
   __shared__ float row_m[kWarps][R], row_l[kWarps][R];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  // (the broadcast tells the compiler that the warp's number is the same in all its lanes)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
   griddep_wait();
   griddep_launch_dependents();
@@ -359,10 +368,29 @@ cache_attend_kernel(const Level a) {
 
   uint8_t* ring = smem + warp * C::kRing;
   const uint32_t ring_addr = smem_u32(ring);
-  // what this lane copies of 16 tokens, from the row of the first
-  const uint8_t* k_src = a.cache.half[0].codes + g * RB + t * C::CPB;
-  const uint8_t* v_src = a.cache.half[1].codes + 2 * t * RB +
-                         (C::VGB < 4 ? (g >> 1) * 4 : g * C::VGB);
+  // this lane copies chunks lane, lane + 32, .. of the 16 tokens' codes
+  const uint8_t* k_src = a.cache.half[0].codes + 16 * lane;
+  const uint8_t* v_src = a.cache.half[1].codes + 16 * lane;
+  uint32_t copy_at[C::kCopies];
+#pragma unroll
+  for (int j = 0; j < C::kCopies; ++j) {
+    const int c = lane + 32 * j, r = c / (RB / 16);
+    copy_at[j] = ring_addr + r * RB + ((c % (RB / 16)) ^ swizzle<RB>(r)) * 16;
+  }
+  // what it reads of a stage: of K, piece p of the row of slot g at k_at ^ (4 CPB p), of slot g + 8
+  // 8 rows on; of V, its share of group gr of the row of slot 2t + (h & 1), at v_at[h & 1] ^
+  // (bytes of a group gr)
+  const int k_tok = slot_token(g);
+  const uint32_t k_at = k_tok * RB + ((t * C::CPB / 16) ^ swizzle<RB>(k_tok)) * 16 + t * C::CPB % 16;
+  uint32_t v_at[2];
+  {
+    const int byte = C::VGB < 4 ? (g >> 1) * 4 : g * C::VGB;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = slot_token(2 * t + h);
+      v_at[h] = C::kK + r * RB + ((byte / 16) ^ swizzle<RB>(r)) * 16 + byte % 16;
+    }
+  }
   // scales and zeros of the 16 tokens: 6 G pieces of 16 bytes, a lane a piece
   const bool grid_lane = lane < 6 * G;
   const uint8_t* g_src;
@@ -423,41 +451,30 @@ cache_attend_kernel(const Level a) {
                                   : make_uint4(0, 0, 0, 0);
     }
 
-    uint32_t put = ring_addr;             // the stage that is filled next
+    uint32_t put = 0;                     // the stage that is filled next
     uint32_t haves = 0;                   // bit k: the k-th last step issued has a page
+    const uint32_t g_dst = ring_addr + 2 * C::kK + 16 * lane;
     auto issue = [&](int i) {
-      haves <<= 1;
-      if (i < steps) {
-        const int32_t page = __shfl_sync(0xffffffffu, pages_now, i & 31);
-        if (page >= 0) {
-          // rows / 16 of the cache stay below 2^31
-          const uint32_t off = (first + i * kTile) & ((1 << a.cache.page_shift) - 1);
-          const uint32_t row16 = ((static_cast<uint32_t>(page) * a.cache.heads + head)
-                                  << (a.cache.page_shift - 4)) + (off >> 4);
-          const uint8_t* k0 = k_src + static_cast<uint64_t>(row16) * (16 * RB);
-          const uint8_t* v0 = v_src + static_cast<uint64_t>(row16) * (16 * RB);
+      const int32_t page = __shfl_sync(0xffffffffu, pages_now, i & 31);
+      const bool have = i < steps && page >= 0;
+      // rows / 16 of the cache stay below 2^31
+      const uint32_t off = (first + i * kTile) & ((1 << a.cache.page_shift) - 1);
+      const uint32_t row16 =
+          ((static_cast<uint32_t>(page) * a.cache.heads + head) << (a.cache.page_shift - 4)) +
+          (off >> 4);
+      const uint8_t* k0 = k_src + static_cast<uint64_t>(row16) * (16 * RB);
+      const uint8_t* v0 = v_src + static_cast<uint64_t>(row16) * (16 * RB);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int p = 0; p < C::NPS; ++p)
-              cp_async(put + lane * C::CPB + (h * C::NPS + p) * 32 * C::CPB,
-                       k0 + 8 * h * RB + p * 4 * C::CPB, C::CPB);
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-#pragma unroll
-            for (int gr = 0; gr < G; ++gr)
-              cp_async(put + lane * C::VB + C::kK + (h * G + gr) * 32 * C::VB,
-                       v0 + ((h & 1) + 8 * (h >> 1)) * RB + gr * (GROUP * BITS / 8), C::VB);
-          if (grid_lane)
-            cp_async(put + C::kK + C::kV + 16 * lane,
-                     g_src + static_cast<uint64_t>(row16) * g_row16, 16);
-          haves |= 1u;
-        }
-        put = put + C::kStage == ring_addr + C::kRing ? ring_addr : put + C::kStage;
-        if ((i & 31) == 31) {      // the next step's page is in the next batch
-          pages_now = pages_next;
-          pages_next = pages_from(i + 33);
-        }
+      for (int j = 0; j < C::kCopies; ++j) {
+        cp_async16(copy_at[j] + put, k0 + 512 * j, have);
+        cp_async16(copy_at[j] + put + C::kK, v0 + 512 * j, have);
+      }
+      cp_async16(g_dst + put, g_src + static_cast<uint64_t>(row16) * g_row16, have && grid_lane);
+      haves = haves << 1 | have;
+      put = put == (kStages - 1) * C::kStage ? 0 : put + C::kStage;
+      if ((i & 31) == 31 && i < steps) {      // the next step's page is in the next batch
+        pages_now = pages_next;
+        pages_next = pages_from(i + 33);
       }
       cp_commit();
     };
@@ -544,7 +561,7 @@ cache_attend_kernel(const Level a) {
       }
     }
 
-    const uint8_t* st = ring;             // the stage that is consumed
+    uint32_t get = 0;                     // the stage that is consumed
     for (int i = 0; i < steps; ++i) {
       cp_wait<kStages - 2>();
       // every lane's copies have landed, and every lane is done with the step before, whose stage
@@ -552,11 +569,12 @@ cache_attend_kernel(const Level a) {
       __syncwarp();
       issue(i + kStages - 1);
       const bool have = haves >> (kStages - 1) & 1u;
+      const uint8_t* st = ring + get;
       const int pos = first + i * kTile;
 
-      // grids of tokens g and g + 8
+      // grids of slots g and g + 8
       float sk[2][G], nz[2][G], ratio_v[2][G], ls[2], rs[2];
-      const uint8_t* grids = st + C::kK + C::kV;
+      const uint8_t* grids = st + 2 * C::kK;
       const uint8_t* zvp = grids + 80 * G;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -564,7 +582,7 @@ cache_attend_kernel(const Level a) {
         float sv[G];
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
-          const int at = (g + 8 * h) * G + gr;
+          const int at = (k_tok + 8 * h) * G + gr;
           sk[h][gr] = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(grids)[at]);
           nz[h][gr] = -static_cast<float>((grids + 32 * G)[at]);
           sv[gr] = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(grids + 48 * G)[at]);
@@ -596,8 +614,8 @@ cache_attend_kernel(const Level a) {
         for (int pp = 0; pp < C::NPS / G; ++pp) {
           const int p = gr * (C::NPS / G) + pp;
           uint32_t wa[C::CPB / 4], wb[C::CPB / 4];
-          const uint8_t* pa = st + (p * 32 + lane) * C::CPB;
-          const uint8_t* pb = st + ((C::NPS + p) * 32 + lane) * C::CPB;
+          const uint8_t* pa = st + (k_at ^ (4 * C::CPB * p));
+          const uint8_t* pb = pa + 8 * RB;
           if constexpr (C::CPB == 16) {
             *reinterpret_cast<uint4*>(wa) = *reinterpret_cast<const uint4*>(pa);
             *reinterpret_cast<uint4*>(wb) = *reinterpret_cast<const uint4*>(pb);
@@ -663,7 +681,7 @@ cache_attend_kernel(const Level a) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            on[nt][e] = have && pos + g + 8 * (e >> 1) <
+            on[nt][e] = have && pos + k_tok + 8 * (e >> 1) <
                                     limit_of(row_first + nt * 8 + 2 * t + (e & 1));
         weigh<D, NT, true>(p, m, l, o, rs, on);
 #pragma unroll
@@ -687,19 +705,18 @@ cache_attend_kernel(const Level a) {
 #pragma unroll
       for (int gr = 0; gr < G; ++gr) {
         uint32_t w[4][C::VB / 4];
-        // zero points of tokens 2t and 2t + 1, and of the two eight further on, as fp16 codes
+        // minus the zero points of slots 2t and 2t + 1, and of the two eight further on, as fp16
+        // codes: rows of an operand whose product with the weights takes the zero points out
         uint32_t zp[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint8_t* z = zvp + (2 * t + 8 * h) * G + gr;
-          if constexpr (G == 1)
-            zp[h] = __byte_perm(*reinterpret_cast<const uint16_t*>(z), 0, 0x4140);
-          else
-            zp[h] = z[0] | static_cast<uint32_t>(z[G]) << 16;
+          const uint8_t* z = zvp + (2 * t + 8 * h) * G + gr;       // tokens 2t and 2t + 1
+          const uint32_t z0 = z[0], z1 = z[G];
+          zp[h] = (t & 1 ? z1 | z0 << 16 : z0 | z1 << 16) | 0x80008000u;
         }
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          const uint8_t* pv = st + C::kK + ((h * G + gr) * 32 + lane) * C::VB;
+          const uint8_t* pv = st + (v_at[h & 1] ^ (gr * (GROUP * BITS / 8))) + (h >> 1) * 8 * RB;
           if constexpr (C::VB == 16)
             *reinterpret_cast<uint4*>(w[h]) = *reinterpret_cast<const uint4*>(pv);
           else if constexpr (C::VB == 8)
@@ -734,18 +751,16 @@ cache_attend_kernel(const Level a) {
               a2 = prmt(ev[2], ev[3], s0) & 0x00FF00FFu;
               a3 = prmt(od[2], od[3], s1) & 0x00FF00FFu;
             }
-            a0 = sub_f16x2(a0, zp[0]);
-            a1 = sub_f16x2(a1, zp[0]);
-            a2 = sub_f16x2(a2, zp[1]);
-            a3 = sub_f16x2(a3, zp[1]);
             const int tile = gr * (GROUP / 16) + wi * kPairs + i2;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16(o[nt][tile], zp[0], zp[0], zp[1], zp[1], bf[nt][gr][0], bf[nt][gr][1]);
               mma_f16(o[nt][tile], a0, a1, a2, a3, bf[nt][gr][0], bf[nt][gr][1]);
+            }
           }
         }
       }
-      st = st + C::kStage == ring + C::kRing ? ring : st + C::kStage;
+      get = get == (kStages - 1) * C::kStage ? 0 : get + C::kStage;
     }
     cp_wait<0>();
 
