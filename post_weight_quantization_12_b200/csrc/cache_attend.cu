@@ -144,8 +144,20 @@ struct Find {
 };
 struct Cut {
   int64_t total, parts;
+  int64_t each;                 // tiles of a run, rounded down
+  uint32_t more;                // and how many there are besides
+  __device__ __forceinline__ Cut(int64_t tiles) {
+    total = tiles;
+    const uint32_t n = min(static_cast<uint64_t>(max(tiles, static_cast<int64_t>(1))),
+                           static_cast<uint64_t>(gridDim.x));
+    parts = n;
+    // (a division of 64-bit numbers takes longer than everything else here)
+    each = tiles >> 32 ? tiles / n : static_cast<uint32_t>(tiles) / n;
+    more = static_cast<uint32_t>(tiles - each * n);
+  }
+  // The first `more` runs have one tile more.
   __device__ __forceinline__ int64_t begin(int64_t part) const {
-    return total / parts * part + total % parts * part / parts;
+    return each * part + min(part, static_cast<int64_t>(more));
   }
 };
 template <int R>
@@ -171,12 +183,12 @@ __device__ __forceinline__ Cut find_tile(const Level& a, int64_t part, Find& sh)
     total += sh.warp_sum[w];
   }
   incl += before;
-  const Cut cut{total, max(min(total, static_cast<int64_t>(gridDim.x)), static_cast<int64_t>(1))};
+  const Cut cut(total);
   const int64_t begin = part < cut.parts ? cut.begin(part) : total;
   if (incl - sum <= begin && begin < incl) {
     int64_t base = incl - sum;
     int64_t b = b0;
-    for (; b + 1 < b1; ++b) {
+    for (; b + 1 < b1; ++b) {       // not entered where a thread has one sequence
       const int64_t t = get_sequence<R>(a, b).tiles;
       if (begin < base + t) break;
       base += t;
@@ -862,10 +874,9 @@ cache_attend_kernel(const Level a) {
 }
 
 // Joins the partial results of the item that starts in run blockIdx.x and ends in a later one: slot
-// 2 c + 1 of its first run c, slots 2 c' of the runs after it. gridDim.y CTAs share the rows of the
-// item, so few long sequences still keep many SMs busy; the warps of a row share its slots.
-constexpr int kJoinWarps = 8;
-template <int D, int R>
+// 2 c + 1 of its first run c, slots 2 c' of the runs after it. The warps share the rows of the item,
+// and with more warps than rows the slots of a row.
+template <int D, int R, int kJoinWarps>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 cache_join_kernel(const Level a) {
   __shared__ float sh[kJoinWarps][D];
@@ -880,11 +891,11 @@ cache_join_kernel(const Level a) {
   const int64_t row0 = __ldcg(join + 4);
   const int row_first = __ldcg(join + 5);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rows_here = R / gridDim.y;
-  const int per_row = max(1, kJoinWarps / rows_here);     // warps of a row
+  constexpr int rows_here = R;
+  constexpr int per_row = kJoinWarps / R < 1 ? 1 : kJoinWarps / R;     // warps of a row
   constexpr int kVec = D / 32;                            // dims of a lane: 2 or 4
   for (int rr = warp / per_row; rr < rows_here; rr += kJoinWarps / per_row) {
-    const int r = blockIdx.y * rows_here + rr, sub = warp % per_row;
+    const int r = rr, sub = warp % per_row;
     float m = kNegInf, l = 0.f, acc[kVec];
 #pragma unroll
     for (int k = 0; k < kVec; ++k) acc[k] = 0.f;
@@ -1003,9 +1014,12 @@ gptq_status attend_level(Level a, cudaStream_t stream) {
       launch_pdl(cache_attend_kernel<D, BITS, GROUP, NT>, dim3(static_cast<unsigned>(grid)),
                  dim3(kThreads), C::kSmem, stream, a);
   if (st != GPTQ_OK || per == 1) return st;    // items of one tile are never shared
-  const unsigned y = items < num_sms() ? C::R : 1;
-  return launch_pdl(cache_join_kernel<D, C::R>, dim3(static_cast<unsigned>(grid), y),
-                    dim3(32 * kJoinWarps), 0, stream, a);
+  // Items of many runs each (few, long sequences): several warps to a row. 131,072 tokens over 8
+  // heads are joined from 74 runs a head.
+  return grid >= 8 * items ? launch_pdl(cache_join_kernel<D, C::R, 32>,
+                                        dim3(static_cast<unsigned>(grid)), dim3(1024), 0, stream, a)
+                           : launch_pdl(cache_join_kernel<D, C::R, 8>,
+                                        dim3(static_cast<unsigned>(grid)), dim3(256), 0, stream, a);
 }
 
 size_t slots_bytes(int dim) {
