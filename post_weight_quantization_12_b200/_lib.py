@@ -136,7 +136,7 @@ def _stream(stream):
     import torch
     if stream is None:
         return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    if isinstance(stream, torch.cuda.Stream):
+    if type(stream) is not int and isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
 
@@ -317,8 +317,10 @@ def cache_append(cache, rows, K, V, K_hat=None, V_hat=None, info=None, stream=No
         raise ValueError("K and V must have the same shape and type")
     _same_rows(K_hat, K, "K_hat")
     _same_rows(V_hat, V, "V_hat")
-    st = load().gptq_cache_append(cache, rows, _ptr(K), ldk, _ptr(V), ldv, _dtype_code(K),
-                                  _ptr(K_hat), _ptr(V_hat), _ptr(info), _stream(stream))
+    st = load().gptq_cache_append(cache, rows, K.data_ptr(), ldk, V.data_ptr(), ldv, _dtype_code(K),
+                                  None if K_hat is None else K_hat.data_ptr(),
+                                  None if V_hat is None else V_hat.data_ptr(), _ptr(info),
+                                  _stream(stream))
     _check(st, "gptq_cache_append")
 
 
@@ -351,8 +353,8 @@ def cache_attend(cache, rows, Q, out, ratio, scale, ws, info=None, stream=None, 
         raise TypeError("Q and out must be bfloat16")
     if out.shape != Q.shape:
         raise ValueError("Q and out must have the same shape")
-    tail = (_ptr(Q), ldq, int(ratio), float(scale), _ptr(out), ldo, _ptr(ws),
-            ws.numel() * ws.element_size(), _ptr(info), _stream(stream))
+    tail = (Q.data_ptr(), ldq, ratio, scale, out.data_ptr(), ldo, ws.data_ptr(), ws.nbytes,
+            _ptr(info), _stream(stream))
     if prefix_len is None:
         _check(load().gptq_cache_attend(cache, rows, *tail), "gptq_cache_attend")
     else:

@@ -271,6 +271,7 @@ class QuantizedCache:
         self.bits, self.group = 32 * words // dim, dim // groups
         self.device = codes.device      # with its index: a tensor's device always has one
         self.info = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._ws_bytes = {}             # workspace sizes by (rows, ratio, shared)
         self._c = _lib.Cache(*(t.data_ptr() for t in tensors), pages, heads, page, dim, self.bits,
                              self.group)
 
@@ -322,7 +323,12 @@ class QuantizedCache:
 
         def call(s):
             o = torch.empty(Q.shape, dtype=Q.dtype, device=self.device) if out is None else out
-            size = _lib.cache_workspace_size(self._c, n, ratio, prefix_len is not None)
+            key = (n, ratio, prefix_len is not None)
+            size = self._ws_bytes.get(key)
+            if size is None:
+                if len(self._ws_bytes) >= 1024:
+                    self._ws_bytes.clear()
+                size = self._ws_bytes[key] = _lib.cache_workspace_size(self._c, *key)
             ws = torch.empty(size, dtype=torch.uint8, device=self.device)
             _lib.cache_attend(self._c, _lib.cache_rows(n, table, lengths, starts), Q, o, ratio,
                               self.dim ** -0.5 if scale is None else scale, ws, self.info, s,

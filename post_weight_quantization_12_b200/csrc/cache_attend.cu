@@ -439,12 +439,18 @@ cache_attend_kernel(const Level a) {
         min(static_cast<int64_t>(limit_hi), (static_cast<int64_t>(tile0) + run) * kTile));
     const int first = tok_begin + kStep * warp;
     const int steps = stop > first ? (stop - first + kTile - 1) / kTile : 0;
-    auto pages_from = [&](int i) -> int32_t {
-      const int k = i + lane;
-      return k < steps ? find_page(a.cache, table, first + static_cast<int64_t>(k) * kTile, a.info)
-                       : -1;
+    // entries of the page table, checked once they have come in (checked()): the loads that follow
+    // need not wait for them
+    auto entry_of = [&](int i) -> int32_t {
+      const int64_t k = (first + static_cast<int64_t>(i + lane) * kTile) >> a.cache.page_shift;
+      return i + lane < steps && k < a.cache.width ? __ldg(table + k) : -1;
     };
-    int32_t pages_now = pages_from(0), pages_next = steps > 32 ? pages_from(32) : -1;
+    auto checked = [&](int i, int32_t p) -> int32_t {
+      const bool ok = p >= 0 && p < a.cache.pages;
+      if (!ok && i + lane < steps) record_info(a.info, GPTQ_INFO_BAD_PAGE);
+      return ok ? p : -1;
+    };
+    int32_t entry = entry_of(0);
 
     // the queries' loads go out while the pages come in
     constexpr int CPD = D / 4 / C::NPS;   // dims of a piece
@@ -463,6 +469,8 @@ cache_attend_kernel(const Level a) {
                                   : make_uint4(0, 0, 0, 0);
     }
 
+    int32_t pages_now = checked(0, entry);        // of steps 0 .. 31 by lane, then of 32 .. 63, ..
+    entry = entry_of(32);                         // the next 32, not checked
     uint32_t put = 0;                     // the stage that is filled next
     uint32_t haves = 0;                   // bit k: the k-th last step issued has a page
     const uint32_t g_dst = ring_addr + 2 * C::kK + 16 * lane;
@@ -485,8 +493,8 @@ cache_attend_kernel(const Level a) {
       haves = haves << 1 | have;
       put = put == (kStages - 1) * C::kStage ? 0 : put + C::kStage;
       if ((i & 31) == 31 && i < steps) {      // the next step's page is in the next batch
-        pages_now = pages_next;
-        pages_next = pages_from(i + 33);
+        pages_now = checked(i + 1, entry);
+        entry = entry_of(i + 33);
       }
       cp_commit();
     };

@@ -812,9 +812,9 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const Merge a) {
   const int qh = blockIdx.y * 8 + (threadIdx.x >> 5);
   const int64_t tok = blockIdx.x, v = tok * per_row + qh;
   if (qh >= per_row) return;
+  // (checked where the result is stored: the loads do not wait for it)
   const int64_t first = a.starts ? __ldg(a.starts) : 0;
   const int64_t end = a.starts ? __ldg(a.starts + a.batch) : a.batch;
-  if (tok < first || tok >= end) return;       // not a row of any sequence: left as it is
   const int head = qh / a.ratio;
   const int64_t j = tok * a.ratio + (qh - head * a.ratio);
   const int64_t ri = j >> 8;
@@ -824,19 +824,17 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const Merge a) {
   const int parts = two ? a.splits : 2 * a.splits;
   const int wg = two ? r >> 7 : 0;
   r &= 127;
-  float m = __ldcg(a.mid_lse + v), l = 0.f, acc[kVec];
+  const float mid_lse = __ldcg(a.mid_lse + v);
+  float mid[kVec];
+  if constexpr (kVec == 4)
+    *reinterpret_cast<float4*>(mid) =
+        __ldcg(reinterpret_cast<const float4*>(a.mid + v * D + lane * kVec));
+  else
+    *reinterpret_cast<float2*>(mid) =
+        __ldcg(reinterpret_cast<const float2*>(a.mid + v * D + lane * kVec));
+  float m = kNegInf, l = 0.f, acc[kVec];
 #pragma unroll
   for (int k = 0; k < kVec; ++k) acc[k] = 0.f;
-  if (m != kNegInf) {
-    l = 1.f;
-    const float* src = a.mid + v * D + lane * kVec;
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) acc[k] = __ldcg(src + k);
-    if (!(m > kNegInf)) {        // NaN: keep it in the values, and a reference that compares
-      m = 0.f;
-      l = NAN;
-    }
-  }
   constexpr int kAhead = 12;
   for (int s0 = 0; s0 < parts; s0 += kAhead) {
     float x[kAhead][kVec], lse[kAhead];
@@ -863,6 +861,13 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const Merge a) {
       for (int d = 0; d < kVec; ++d) acc[d] = fmaf(acc[d], f, w * x[k][d]);
     }
   }
+  if (mid_lse != kNegInf) {
+    const float top = fmaxf(m, mid_lse), ref = top == kNegInf ? 0.f : top;
+    const float f = m == kNegInf ? (l == 0.f ? 0.f : 1.f) : ex2(m - ref), w = ex2(mid_lse - ref);
+    l = fmaf(l, f, w);
+#pragma unroll
+    for (int d = 0; d < kVec; ++d) acc[d] = fmaf(acc[d], f, w * mid[d]);
+  }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint32_t o[kVec / 2];
 #pragma unroll
@@ -870,6 +875,7 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const Merge a) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * k] * inv, acc[2 * k + 1] * inv);
     o[k] = *reinterpret_cast<const uint32_t*>(&h);
   }
+  if (tok < first || tok >= end) return;       // not a row of any sequence: left as it is
   __nv_bfloat16* dst = a.out + tok * a.ldo + static_cast<int64_t>(qh) * D + lane * kVec;
   if constexpr (kVec == 4)
     *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
