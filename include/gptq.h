@@ -427,6 +427,8 @@ typedef struct gptq_cache_rows {
  *                 aligned rows.
  *   K_hat_dev, V_hat_dev  [n][heads * dim] dense, of the same type, or NULL: what the codes stand
  *                 for, s (q - z) (rounded to nearest even for bf16), of the rows that were stored.
+ *                 K_hat_dev may be K_dev itself (and V_hat_dev V_dev) if that is dense; otherwise
+ *                 none of the four may overlap.
  * Two rows of one call must not share a position (sequences that share a page may not write into
  * it): which codes and which grid remain is then not determined.
  * n == 0 enqueues nothing. Errors: GPTQ_EINVAL (shapes, null pointers, alignment, dtype),
@@ -454,15 +456,17 @@ gptq_status gptq_cache_read(const gptq_cache* cache, const gptq_cache_rows* rows
  * meets no position gives 0.
  *   Q_dev, out_dev  [n][heads * ratio * dim] bf16, row strides ldq, ldo (elements, multiples of 8),
  *                   16-byte aligned; they must not overlap.
- *   ratio           query heads per cache head, 1 .. 1024.
+ *   ratio           query heads per cache head, 1 .. 1024; heads * ratio at most 2^18 and n * ratio
+ *                   below 2^31 (GPTQ_EUNSUPPORTED beyond).
  *   scale           usually 1 / sqrt(dim); finite.
  *   ws_dev          gptq_cache_workspace_size(cache, n, ratio, 0) bytes, 256-byte aligned; calls
  *                   that may overlap on the GPU need one each, graphs captured with the same one
  *                   must not be replayed at the same time.
  * Arithmetic: products of fp16 operands with fp32 sums. Codes are exact; the weights are rounded to
- * fp16 (2^-12 of each) relative to the largest, fp32 otherwise; one rounding to bf16 at the end.
- * V scales below 2^-96 lose accuracy relative to themselves. Results do not depend on timing, and
- * are the same again for the same call on the same device.
+ * fp16 (2^-12 of each, or 2^-25 of the largest), fp32 otherwise; one rounding to bf16 at the end.
+ * A token whose V scales all lie below 2^-96 keeps less than fp16's accuracy of them. A NaN scale
+ * gives NaN in what meets it: a key's in the row, a value's in its group of dimensions. Results do
+ * not depend on timing, and are the same again for the same call on the same device.
  * n == 0 enqueues nothing. Errors: as gptq_cache_append, GPTQ_EWORKSPACE.
  */
 gptq_status gptq_cache_attend(const gptq_cache* cache, const gptq_cache_rows* rows,
@@ -475,10 +479,12 @@ gptq_status gptq_cache_attend(const gptq_cache* cache, const gptq_cache_rows* ro
  * the page list prefix_table_dev (ceil(prefix_len / page) entries). Row i meets all of the prefix
  * and then its own sequence as in gptq_cache_attend (lengths count the own positions only; they may
  * be 0). The prefix is met by the rows of all sequences together, so its codes are read and
- * unpacked once per 128 or so rows instead of once per sequence.
+ * unpacked once per 256 rows of a cache head (once per 16 of up to 32) instead of once per sequence.
  *   prefix_len      0 .. 2^30, on the host.
  *   ws_dev          gptq_cache_workspace_size(cache, n, ratio, 1) bytes.
- * Other arguments, arithmetic and errors as gptq_cache_attend.
+ * Arithmetic of the prefix for more than 32 rows (n * ratio): its keys and values become fp16 (2^-12
+ * of each, or 2^-32 of the largest near it) before the products. Other arguments, arithmetic and
+ * errors as gptq_cache_attend.
  */
 gptq_status gptq_cache_attend_shared(const gptq_cache* cache, const gptq_cache_rows* rows,
                                      const int32_t* prefix_table_dev, int64_t prefix_len,

@@ -338,6 +338,11 @@ gptq_status gptq_cache_append(const gptq_cache* cache, const gptq_cache_rows* ro
   if (K_dev == nullptr || V_dev == nullptr || !aligned(K_dev, 16) || !aligned(V_dev, 16) ||
       !aligned(K_hat_dev, 16) || !aligned(V_hat_dev, 16))
     return GPTQ_EINVAL;
+  // in place only where the rows of both lie alike
+  if ((K_hat_dev == K_dev && ldk != width) || (V_hat_dev == V_dev && ldv != width))
+    return GPTQ_EINVAL;
+  if (K_hat_dev != nullptr && (K_hat_dev == V_hat_dev || K_hat_dev == V_dev)) return GPTQ_EINVAL;
+  if (V_hat_dev != nullptr && V_hat_dev == K_dev) return GPTQ_EINVAL;
   return run_cache_append(c, r, cache->dim, cache->bits, cache->group, K_dev, ldk, V_dev, ldv,
                           dtype == GPTQ_BF16, K_hat_dev, V_hat_dev, info_dev,
                           static_cast<cudaStream_t>(stream));
@@ -353,8 +358,7 @@ gptq_status gptq_cache_read(const gptq_cache* cache, const gptq_cache_rows* rows
     return st;
   if (dtype != GPTQ_BF16 && dtype != GPTQ_FP32) return GPTQ_EINVAL;
   if (r.n == 0 || r.batch == 0) return GPTQ_OK;
-  if ((K_out_dev == nullptr && V_out_dev == nullptr) || !aligned(K_out_dev, 16) ||
-      !aligned(V_out_dev, 16))
+  if (K_out_dev == V_out_dev || !aligned(K_out_dev, 16) || !aligned(V_out_dev, 16))
     return GPTQ_EINVAL;
   return run_cache_read(c, r, cache->dim, cache->bits, cache->group, K_out_dev, V_out_dev,
                         dtype == GPTQ_BF16, info_dev, static_cast<cudaStream_t>(stream));

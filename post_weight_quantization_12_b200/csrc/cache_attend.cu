@@ -793,7 +793,7 @@ cache_attend_kernel(const Level a) {
         for (int off = 4; off < 32; off <<= 1) {
           l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], off);
         }
-    __syncthreads();       // the rings are idle, and the last item's results have been read
+    __syncthreads();       // the rings are idle
     float* res = reinterpret_cast<float*>(smem) + warp * R * C::kPad;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -866,6 +866,7 @@ cache_attend_kernel(const Level a) {
     }
     // ---- the next item ----
     cur += run;
+    if (cur < end) __syncthreads();   // its copies overwrite the results just read
     tile0 = 0;
     item0 = cur;
     if (++rt == s.row_tiles) {
@@ -1081,7 +1082,11 @@ gptq_status run_cache_attend(const CacheView& c, const CacheRows& r, int dim, in
     const size_t rows = static_cast<size_t>(r.n) * c.heads * q.ratio;
     a.mid_lse = reinterpret_cast<float*>(w);
     a.mid = reinterpret_cast<float*>(w + align_up(rows * 4, 256));
-    if (r.n * q.ratio > 16) {
+    // A second or third row tile of 16 costs a second pass over the codes; the tensor-core kernel
+    // costs the same for up to 128 rows. Over 32,768 tokens x 32 heads of 4-bit codes: 32 rows
+    // 124 us here and 159 us there, 48 rows 169 and 157, 128 rows 400 and 171; over 1000 tokens
+    // the two are within 4 us of each other from 20 to 128 rows.
+    if (r.n * q.ratio > 32) {
       w += align_up(rows * 4, 256) + align_up(rows * dim * 4, 256);
       a.out = nullptr;
       const gptq_status st = level(a, (r.n * q.ratio + r.batch - 1) / r.batch);

@@ -316,7 +316,8 @@ cache_prefix_kernel(const Prefix a) {
         tc_fence_after();
         const int slot = gs & 3;
         const int e_new = v_exp[slot];
-        const float xs = row_c * pow2(k_exp[slot]);
+        // (never 0: a token that does not count has a product of -inf)
+        const float xs = fmaxf(row_c * pow2(k_exp[slot]), 1.17549435e-38f);
         const uint32_t ts = tm_s(i) + lane_base;
         uint32_t va[16], vb[16];
         const uint4 vm = *reinterpret_cast<const uint4*>(valid[slot]);

@@ -61,11 +61,11 @@ def dev(a):
 
 
 def check_attend(out, host, table, lengths, starts, q, scale, prefix=None, image16=False,
-                 rows=None):
+                 rows=None, flip=1.0):
     """Compares rows of `out` [n, q_heads, dim] with the oracle's within its derived bound. prefix:
-    (table row, length) that every row meets first."""
+    (table row, length) that every row meets first; flip: a negative or zero scale's sign."""
     out = out.double().cpu().numpy()
-    qf = q.double().cpu().numpy()
+    qf = q.double().cpu().numpy() * np.sign(flip)
     ratio = q.shape[1] // host.heads
     for b in range(len(lengths)):
         for i in range(starts[b], starts[b + 1]):

@@ -76,6 +76,12 @@ def test_bad_tensors(built_lib):
     assert append(k=None) == E and append(v=None) == E
     assert append(ldk=128) == E and append(ldv=252) == E and append(ldk=260) == E
     assert append(dtype=7) == E and append(k=0x80008) == E and append(kh=0x80008) == E
+    # in place only if dense; outputs distinct from everything else
+    assert append(k=0x80000, kh=0x80000, ldk=512) == E
+    assert append(kh=0xB0000, vh=0xB0000) == E and append(kh=0x90000) == E
+    assert append(vh=0x80000) == E and read(k=0x80000, v=0x80000) == E
+    assert attend(c=cache(heads=1024), ratio=512, ldq=1 << 27, ldo=1 << 27) == U
+    assert attend(r=rows(n=1 << 22), ratio=1000, ldq=1 << 20, ldo=1 << 20) == U
     assert read(k=None, v=None) == E and read(dtype=9) == E and read(k=0x80004) == E
     assert attend(q=None) == E and attend(out=None) == E and attend(q=0x90000) == E
     assert attend(ldq=256) == E and attend(ldo=514) == E and attend(ratio=0) == E

@@ -173,6 +173,21 @@ def test_append_from_a_fused_projection():
         assert torch.count_nonzero(getattr(a, part)) > 0
 
 
+def test_append_in_place():
+    """The stored values written over the dense inputs."""
+    lengths, starts = np.array([40], np.int32), np.array([0, 40], np.int32)
+    table = np.array([[1, 2, 0]], np.int32)
+    g = torch.Generator().manual_seed(12)
+    K, V = (torch.randn(40, 5, 64, generator=g) for _ in range(2))
+    a, b = K.to(DEV), V.to(DEV)
+    cache = api.QuantizedCache(3, 5, 64, 16, 4, 32)
+    cache.append(a, b, dev(table), dev(lengths), dev(starts), K_hat=a, V_hat=b)
+    torch.cuda.synchronize()
+    for x, got in ((K, a), (V, b)):
+        want = oracle.cache_values(*oracle.grid_quantize(x.numpy(), 4, 32))
+        assert torch.equal(got.cpu(), torch.from_numpy(want).float())
+
+
 def test_rows_behind_the_last_sequence_are_ignored():
     """A padded batch: rows from starts[batch] on change neither the cache nor the outputs."""
     lengths, starts = np.array([4, 9], np.int32), np.array([0, 3, 5], np.int32)

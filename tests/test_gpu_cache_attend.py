@@ -119,6 +119,59 @@ def test_queries_of_any_magnitude():
     _run(host, [40], [1], 1, q=q, scale=2.0 ** -103)
 
 
+@pytest.mark.parametrize("scale", [0.0, -0.125, 1e-6])
+def test_any_scale(scale):
+    host = HostCache(30, 1, 16, 128, 4, 128, seed=22)
+    q = _q(3, 4, 128, 9)
+    lengths, starts = np.array([100, 37], np.int32), np.array([0, 1, 3], np.int32)
+    table = make_table(lengths, 16, 30, 1, first=9)
+    cache = host.device()
+    out = cache.attend(q.to(DEV), dev(table), dev(lengths), dev(starts), scale=scale)
+    torch.cuda.synchronize()
+    check_attend(out, host, table, lengths, starts, q, abs(scale) or 1.0, flip=scale)
+    q = _q(40, 4, 128, 10)
+    starts = np.array([0, 17, 40], np.int32)
+    ptable = np.arange(9, dtype=np.int32)
+    out = cache.attend_shared(q.to(DEV), dev(ptable), 140, dev(table), dev(lengths), dev(starts),
+                              scale=scale)
+    torch.cuda.synchronize()
+    check_attend(out, host, table, lengths, starts, q, abs(scale) or 1.0, flip=scale,
+                 prefix=(ptable, 140), image16=True, rows={0, 16, 20, 39})
+
+
+def test_a_cache_past_four_gigabytes():
+    """Pages whose codes lie 5 GB into the tensors: written, read, attended to, as a prefix too."""
+    heads, dim, page = 8, 128, 64
+    pages = 5 * 2 ** 30 // (heads * page * dim) + 8
+    t = [torch.empty(pages, heads, page, n, dtype=dt, device=DEV) for _ in range(2)
+         for n, dt in ((dim // 4, torch.int32), (1, torch.bfloat16), (1, torch.uint8))]
+    cache = api.QuantizedCache.of_tensors(*t, dim=dim)
+    g = torch.Generator().manual_seed(11)
+    K, V = (torch.randn(100, heads, dim, generator=g).to(torch.bfloat16) for _ in range(2))
+    table = np.array([[pages - 1, pages - 3]], np.int32)
+    lengths, starts = np.array([100], np.int32), np.array([0, 100], np.int32)
+    hat = [torch.empty_like(K, device=DEV) for _ in range(2)]
+    cache.append(K.to(DEV), V.to(DEV), dev(table), dev(lengths), dev(starts), *hat)
+    back = cache.read(dev(table), dev(lengths), dev(starts), n=100)
+    torch.cuda.synchronize()
+    assert torch.equal(back[0], hat[0]) and torch.equal(back[1], hat[1])
+    parts = [oracle.grid_quantize(x.float().numpy(), 8, dim) for x in (K, V)]
+    assert torch.equal(hat[0].cpu(), torch.from_numpy(oracle.cache_values(*parts[0]))
+                       .to(torch.bfloat16))
+    q = _q(1, 16, dim, 12)
+    o1 = cache.attend(q.to(DEV), dev(table), dev(lengths))
+    qs = q.expand(20, -1, -1).contiguous()
+    o2 = cache.attend_shared(qs.to(DEV), dev(table[0]), 100, dev(np.zeros((20, 1), np.int32)),
+                             dev(np.zeros(20, np.int32)))
+    torch.cuda.synchronize()
+    assert int(cache.info.item()) == 0
+    for h in range(16):
+        args = [p[:, h // 2] for part in parts for p in part]
+        for got, image in ((o1[0], False), (o2[0], True), (o2[19], True)):
+            ref, tol = oracle.attend_bound(q[0, h].double().numpy(), *args, dim ** -0.5, image)
+            assert np.all(np.abs(got[h].double().cpu().numpy() - ref) <= tol)
+
+
 def test_slots_behind_a_sequence_hold_anything():
     """NaN scales and garbage past the end, and on pages that are not the sequence's."""
     host = HostCache(6, 2, 16, 128, 4, 128, seed=16)
