@@ -483,3 +483,18 @@ def test_decode_steps_of_a_quantized_attention_layer():
                                                    dim ** -0.5, image)
                     assert np.all(np.abs(got[b, h].double().cpu().numpy() - ref) <= tol)
     assert int(cache.info.item()) == 0 and torch.isfinite(full).all()
+
+
+def test_an_item_per_warp():
+    """Enough sequences times heads for every warp of the device to work on its own: one, several
+    and no tiles a sequence, items that two warps share, empty sequences between."""
+    heads, batch = 24, 130
+    rng = np.random.default_rng(5)
+    lengths = rng.integers(1, 70, batch)
+    lengths[[0, 7, 64, 129]] = [0, 300, 16, 250]
+    news = np.ones(batch, int)
+    news[[3, 50, 51]] = 0
+    host = HostCache(int(sum(-(-n // 16) for n in lengths)) + 1, heads, 16, 64, 4, 32, seed=50)
+    _run(host, lengths, news, 2, rows={0, 1, 6, 7, 60, 62, 100, 126})
+    news = np.minimum(rng.integers(1, 4, batch), 3)
+    _run(host, lengths, news, 2, rows={0, 1, 2, 14, 15, 100, 200})
