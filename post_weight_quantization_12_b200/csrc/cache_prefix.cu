@@ -17,9 +17,9 @@
 //   warp 0           issues the products: PV(0), QK(0) of the next tile, PV(1), QK(1), so one
 //                    tile's softmax runs under the other's products (the oldest warp: an SM's
 //                    scheduler lets it go first, and every other role waits for it)
-//   warps 4-7, 8-11  softmax of row tile 0 and 1, one thread a row; they also bring Q in and write
-//                    the results
-//   warps 12-15      unpack K and V of the next tiles into two buffers each, loads a tile ahead
+//   warps 4-11, 12-19  softmax of row tile 0 and 1, two threads a row: each takes half of the
+//                    tokens, and half of the dimensions when they bring Q in and write the results
+//   warps 20-23      unpack K and V of the next tiles into two buffers each, loads a tile ahead
 // With no more than 128 rows in an item, both softmax groups take the same rows and every other
 // token tile. The runs' results (row, fp32, with its log-sum) are joined by cache_merge_kernel.
 #include <cuda_runtime.h>
@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kTok = 128;                  // tokens of a tile
 constexpr int kSm0 = 4;                    // the first softmax warp
-constexpr int kDq0 = 12, kDqWarps = 4;      // the unpacking warps
+constexpr int kDq0 = 20, kDqWarps = 4;     // the unpacking warps
 constexpr int kDqRows = kTok / kDqWarps;   // rows of a tile that one of them takes: one a lane
 static_assert(kDqRows == 32, "a lane a row");
 constexpr int kMmaWarp = 0;
@@ -73,29 +73,17 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, 
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
       ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate) : "memory");
 }
-__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
-      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15]), "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};"
                ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
                  "r"(r[7]), "r"(taddr)
                : "memory");
 }
-__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
 // One lane of a converged warp, the same at every call.
 __device__ __forceinline__ bool elect_one() {
@@ -109,11 +97,23 @@ __device__ __forceinline__ void tmem_wait_st() {
 }
 // Waits for the tensor-memory loads issued so far; the registers are named so that nothing that
 // uses them moves ahead of the wait.
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[8]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]),
+                 "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]),
+                 "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]),
+                 "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+                 "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
                :
                : "memory");
 }
@@ -209,19 +209,20 @@ cache_prefix_kernel(const Prefix a) {
   __shared__ __align__(16) uint32_t valid[4][4];   // of step s in slot s % 4: tokens that count
   __shared__ int k_exp[4], v_exp[4];               // ... and the exponents of its images
   __shared__ uint32_t warp_top[2][kDqWarps][2];
+  __shared__ float row_x[2][128];                  // of (row tile, row): what its halves exchange
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&q_full[b], 128);
+      mbar_init(&q_full[b], 256);
       mbar_init(&k_full[b], 32 * kDqWarps);
       mbar_init(&k_empty[b], 1);
       mbar_init(&v_full[b], 32 * kDqWarps);
       mbar_init(&v_empty[b], 1);
       mbar_init(&s_full[b], 1);
-      mbar_init(&p_full[b], 128);
+      mbar_init(&p_full[b], 256);
       mbar_init(&pv_done[b], 1);
     }
     mbar_init(&mma_done, 1);
@@ -236,19 +237,33 @@ cache_prefix_kernel(const Prefix a) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
-  auto tm_s = [&](int i) { return tmem + 128 * i; };             // S, and P over its first half
+  auto tm_s = [&](int i) { return tmem + 128 * i; };   // S; P over the first half of each half
   auto tm_o = [&](int i) { return tmem + 256 + D * i; };
   griddep_wait();
   griddep_launch_dependents();
   int32_t* info = a.info;
 
   if (warp >= kSm0 && warp < kDq0) {
-    // ---- softmax group i, one row a thread ----
-    const int i = (warp - kSm0) >> 2;
-    const int r = threadIdx.x & 127;
+    // ---- softmax group i: threads r and r + 128 of it share row r, tokens 64 hf .. of each tile ----
+    const int i = (warp - kSm0) >> 3, hf = ((warp - kSm0) >> 2) & 1;
+    const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t pair = 2 + i * 4 + (warp & 3);       // the barrier of the two warps of a row
+    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory"); };
+    // the other half's value: one place for both, first for the one, then for the other
+    auto exchange = [&](float x) -> float {
+      if (hf == 0) row_x[i][r] = x;
+      pair_sync();
+      const float y = row_x[i][r];
+      pair_sync();
+      if (hf == 1) row_x[i][r] = x;
+      pair_sync();
+      const float z = row_x[i][r];
+      pair_sync();
+      return hf == 0 ? z : y;
+    };
     uint32_t c_step = 0;        // steps of this group so far
-    uint32_t g_base = 0;         // steps of the units before
+    uint32_t g_base = 0;        // steps of the units before
     bool ok = true;
     for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
       const Unit w = get_unit(a, u);
@@ -258,18 +273,18 @@ cache_prefix_kernel(const Prefix a) {
       // Q: fp16 after a power of two per row (group 1 writes its own tile only)
       float row_c = 0.f;
       {
-        uint4 raw[D / 8];
+        uint4 raw[D / 16];
         float top = 0.f;
         if (live) {
           const int j = w.row0 + row;
           const int tok = static_cast<int>(static_cast<uint32_t>(j) / static_cast<uint32_t>(a.ratio));
           const uint4* src = reinterpret_cast<const uint4*>(
               a.q + tok * a.ldq +
-              (static_cast<int64_t>(w.head) * a.ratio + (j - tok * a.ratio)) * D);
+              (static_cast<int64_t>(w.head) * a.ratio + (j - tok * a.ratio)) * D + hf * (D / 2));
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) raw[c] = __ldg(src + c);
+          for (int c = 0; c < D / 16; ++c) raw[c] = __ldg(src + c);
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
+          for (int c = 0; c < D / 16; ++c) {
             const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -278,16 +293,16 @@ cache_prefix_kernel(const Prefix a) {
           }
         } else {
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) raw[c] = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < D / 16; ++c) raw[c] = make_uint4(0, 0, 0, 0);
         }
+        top = fmaxf(top, exchange(top));
         const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
         // a negative scale goes into Q, so the largest score is the largest product
         const float up = (e > 127 ? 1.f : pow2(14 - e)) * (a.scale_log2 < 0.f ? -1.f : 1.f);
         row_c = (e > 127 ? 1.f : pow2(e - 14)) * fabsf(a.scale_log2);
         if (w.two || i == 0) {
-          uint8_t* dst = q_tile(i) + r * 128;
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
+          for (int c = 0; c < D / 16; ++c) {
             const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
             float f[8];
 #pragma unroll
@@ -300,67 +315,65 @@ cache_prefix_kernel(const Prefix a) {
                                                    half2_bits(f[2], f[6]), half2_bits(f[3], f[7]))
                                       : make_uint4(half2_bits(f[0], f[1]), half2_bits(f[2], f[3]),
                                                    half2_bits(f[4], f[5]), half2_bits(f[6], f[7]));
-            *reinterpret_cast<uint4*>(dst + (c >> 3) * (kTok * 128) +
-                                      (((c & 7) ^ (r & 7)) << 4)) = h;
+            const int chunk = hf * (D / 16) + c;        // of eight dims
+            *reinterpret_cast<uint4*>(q_tile(i) + r * 128 + (chunk >> 3) * (kTok * 128) +
+                                      (((chunk & 7) ^ (r & 7)) << 4)) = h;
           }
           fence_proxy_async_smem();
           mbar_arrive(&q_full[i]);
         }
       }
-      float m = kNegInf, l = 0.f;
+      float m = kNegInf, l = 0.f;       // of the row; l: this half's share
       int e_ref = -1000;
       for (int k = 0; k < my_steps; ++k, ++c_step) {
-        const uint32_t gs = g_base + step_of(w, i, k);
+        const int slot = (g_base + step_of(w, i, k)) & 3;
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[i], c_step & 1, &abort_flag, info));
-        if (!ok) break;
         tc_fence_after();
-        const int slot = gs & 3;
         const int e_new = v_exp[slot];
         // (never 0: a token that does not count has a product of -inf)
         const float xs = fmaxf(row_c * pow2(k_exp[slot]), 1.17549435e-38f);
-        const uint32_t ts = tm_s(i) + lane_base;
-        uint32_t va[16], vb[16];
-        const uint4 vm = *reinterpret_cast<const uint4*>(valid[slot]);
-        if ((vm.x & vm.y & vm.z & vm.w) != 0xFFFFFFFFu) {
+        const uint32_t ts = tm_s(i) + lane_base + 64 * hf;
+        uint32_t v[32];
+        const uint2 vm = *reinterpret_cast<const uint2*>(&valid[slot][2 * hf]);
+        if ((vm.x & vm.y) != 0xFFFFFFFFu) {
           // tokens that do not count: their products become -inf
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
-            const uint32_t mask = valid[slot][c >> 1] >> (16 * (c & 1));
-            tmem_ld_32x32b_x16(ts + 16 * c, va);
-            tmem_wait_ld(va);
+            const uint32_t mask = (c < 4 ? vm.x : vm.y) >> (8 * (c & 3));
+            uint32_t x[8];
+            tmem_ld_32x32b_x8(ts + 8 * c, x);
+            tmem_wait_ld(x);
 #pragma unroll
-            for (int t = 0; t < 16; ++t)
-              if (!(mask >> t & 1u)) va[t] = __float_as_uint(kNegInf);
-            tmem_st_32x32b_x16(ts + 16 * c, va);
+            for (int t = 0; t < 8; ++t)
+              if (!(mask >> t & 1u)) x[t] = __float_as_uint(kNegInf);
+            tmem_st_32x32b_x8(ts + 8 * c, x);
           }
           tmem_wait_st();
         }
-        // largest product of the row; each load runs under the maxima of the one before
-        float top = kNegInf;
-        auto max16 = [&](const uint32_t (&v)[16]) {
-          float x = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
-          float y = fmaxf(__uint_as_float(v[2]), __uint_as_float(v[3]));
+        // largest product of the row's half: tokens 32 .., then 0 .., which stay in registers
+        float top = kNegInf, top_b = kNegInf;
+        auto max32 = [&]() {
 #pragma unroll
-          for (int t = 4; t < 16; t += 4) {
-            x = fmaxf(fmaxf(x, __uint_as_float(v[t])), __uint_as_float(v[t + 1]));
-            y = fmaxf(fmaxf(y, __uint_as_float(v[t + 2])), __uint_as_float(v[t + 3]));
+          for (int t = 0; t < 32; t += 4) {
+            top = fmaxf(fmaxf(top, __uint_as_float(v[t])), __uint_as_float(v[t + 1]));
+            top_b = fmaxf(fmaxf(top_b, __uint_as_float(v[t + 2])), __uint_as_float(v[t + 3]));
           }
-          top = fmaxf(top, fmaxf(x, y));
         };
-        tmem_ld_32x32b_x16(ts, va);
-#pragma unroll
-        for (int c = 0; c < 8; c += 2) {
-          tmem_wait_ld(va);
-          tmem_ld_32x32b_x16(ts + 16 * c + 16, vb);
-          max16(va);
-          tmem_wait_ld(vb);
-          if (c < 6) tmem_ld_32x32b_x16(ts + 16 * c + 32, va);
-          max16(vb);
-        }
+        tmem_ld_32x32b_x32(ts + 32, v);
+        tmem_wait_ld(v);
+        max32();
+        tmem_ld_32x32b_x32(ts, v);
+        tmem_wait_ld(v);
+        max32();
+        top = fmaxf(top, top_b);
         top = top == kNegInf ? kNegInf : top * xs;
-        const bool grow = top > m + 8.f || (m == kNegInf && top > kNegInf);
-        if (__any_sync(0xffffffffu, grow) || e_new > e_ref) {
-          const float m_new = fmaxf(m, top);
+        // both warps of the rows go one way: on, or through a new reference (or out, after an error).
+        if (named_barrier_or(pair, 64, !ok || top > m + 8.f || e_new > e_ref)) {
+          if (named_barrier_or(pair, 64, !ok)) {
+            ok = false;
+            break;
+          }
+          const float m_new = fmaxf(m, fmaxf(top, exchange(top)));
           const float f = m == kNegInf ? 0.f : ex2(m - m_new);
           l *= f;
           m = m_new;
@@ -368,44 +381,43 @@ cache_prefix_kernel(const Prefix a) {
             // O of the steps so far: the products that made it are complete (they were issued
             // before this step's S)
             const float fo = f * (e_ref < e_new - 120 ? 0.f : pow2(e_ref - e_new));
+            const uint32_t to = tm_o(i) + lane_base + hf * (D / 2);
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
-              tmem_ld_32x32b_x16(tm_o(i) + lane_base + 16 * c, va);
-              tmem_wait_ld(va);
+              uint32_t x[8];
+              tmem_ld_32x32b_x8(to + 8 * c, x);
+              tmem_wait_ld(x);
 #pragma unroll
-              for (int t = 0; t < 16; ++t) va[t] = __float_as_uint(__uint_as_float(va[t]) * fo);
-              tmem_st_32x32b_x16(tm_o(i) + lane_base + 16 * c, va);
+              for (int t = 0; t < 8; ++t) x[t] = __float_as_uint(__uint_as_float(x[t]) * fo);
+              tmem_st_32x32b_x8(to + 8 * c, x);
             }
           }
           e_ref = e_new;
         }
-        // weights, written over the S that they come from (chunk c of 16 over columns 8 c ..,
-        // which have been read by then)
+        // weights, written over the S that they come from: 64 tokens' over the first 32 columns of
+        // their half, of which what is still to be read lies behind
         const float ref = m == kNegInf ? 0.f : m;
         const float2 xs2 = make_float2(xs, xs), ref2 = make_float2(-ref, -ref);
         float2 sum = make_float2(0.f, 0.f), sum_b = sum;
-        auto weigh = [&](const uint32_t (&v)[16], int c) {
-          uint32_t p[8];
+        auto weigh = [&](int c) {
 #pragma unroll
-          for (int t = 0; t < 16; t += 2) {
-            const float2 x =
-                fma2(make_float2(__uint_as_float(v[t]), __uint_as_float(v[t + 1])), xs2, ref2);
-            const float2 w = make_float2(ex2(x.x), ex2(x.y));
-            if (t & 2) sum = add2(sum, w); else sum_b = add2(sum_b, w);
-            p[t / 2] = half2_bits(w.x, w.y);
+          for (int x = 0; x < 2; ++x) {
+            uint32_t p[8];
+#pragma unroll
+            for (int t = 0; t < 16; t += 2) {
+              const float2 y = fma2(make_float2(__uint_as_float(v[16 * x + t]),
+                                                __uint_as_float(v[16 * x + t + 1])), xs2, ref2);
+              const float2 e = make_float2(ex2(y.x), ex2(y.y));
+              if (t & 2) sum = add2(sum, e); else sum_b = add2(sum_b, e);
+              p[t / 2] = half2_bits(e.x, e.y);
+            }
+            tmem_st_32x32b_x8(ts + 16 * c + 8 * x, p);
           }
-          tmem_st_32x32b_x8(ts + 8 * c, p);
         };
-        tmem_ld_32x32b_x16(ts, va);
-#pragma unroll
-        for (int c = 0; c < 8; c += 2) {
-          tmem_wait_ld(va);
-          tmem_ld_32x32b_x16(ts + 16 * c + 16, vb);
-          weigh(va, c);
-          tmem_wait_ld(vb);
-          if (c < 6) tmem_ld_32x32b_x16(ts + 16 * c + 32, va);
-          weigh(vb, c + 1);
-        }
+        weigh(0);
+        tmem_ld_32x32b_x32(ts + 32, v);
+        tmem_wait_ld(v);
+        weigh(1);
         sum = add2(sum, sum_b);
         l += sum.x + sum.y;
         tmem_wait_st();
@@ -420,41 +432,41 @@ cache_prefix_kernel(const Prefix a) {
       if (my_steps > 0) {
         ok = __all_sync(0xffffffffu,
                         mbar_wait_bounded(&pv_done[i], (c_step - 1) & 1, &abort_flag, info));
-        if (!ok) break;
+        if (named_barrier_or(pair, 64, !ok)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
+        l += exchange(l);
         lse = l == 0.f ? kNegInf : (m == kNegInf ? 0.f : m) + log2f(l);
         const float f = l == 0.f ? 0.f : 1.f / l;
         // 2^e_ref in two factors: each within fp32's normal range
         const float f0 = pow2(e_ref / 2), f1 = pow2(e_ref - e_ref / 2);
-        float* dst = a.part + (slot * 128 + r) * D;
+        float* dst = a.part + (slot * 128 + r) * D + hf * (D / 2);
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(tm_o(i) + lane_base + 16 * c, v);
-          tmem_wait_ld(v);
+          uint32_t x[8];
+          tmem_ld_32x32b_x8(tm_o(i) + lane_base + hf * (D / 2) + 8 * c, x);
+          tmem_wait_ld(x);
 #pragma unroll
-          for (int t = 0; t < 16; ++t)
-            v[t] = __float_as_uint(__uint_as_float(v[t]) * f * f0 * f1);
+          for (int t = 0; t < 8; ++t) x[t] = __float_as_uint(__uint_as_float(x[t]) * f * f0 * f1);
           if (live) {
-#pragma unroll
-            for (int t = 0; t < 16; t += 8) {
-              uint4 lo, hi;
-              if constexpr (BITS == 4) {      // columns hold dims 0 4 1 5 2 6 3 7 of each eight
-                lo = make_uint4(v[t], v[t + 2], v[t + 4], v[t + 6]);
-                hi = make_uint4(v[t + 1], v[t + 3], v[t + 5], v[t + 7]);
-              } else {
-                lo = make_uint4(v[t], v[t + 1], v[t + 2], v[t + 3]);
-                hi = make_uint4(v[t + 4], v[t + 5], v[t + 6], v[t + 7]);
-              }
-              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                           ::"l"(dst + 16 * c + t), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w),
-                             "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
+            uint4 lo, hi;
+            if constexpr (BITS == 4) {      // columns hold dims 0 4 1 5 2 6 3 7 of each eight
+              lo = make_uint4(x[0], x[2], x[4], x[6]);
+              hi = make_uint4(x[1], x[3], x[5], x[7]);
+            } else {
+              lo = make_uint4(x[0], x[1], x[2], x[3]);
+              hi = make_uint4(x[4], x[5], x[6], x[7]);
             }
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                         ::"l"(dst + 8 * c), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w),
+                           "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
           }
         }
         tc_fence_before();
       }
-      if (live) a.part_lse[slot * 128 + r] = lse;
+      if (live && hf == 0) a.part_lse[slot * 128 + r] = lse;
     }
   } else if (warp >= kDq0) {
     // ---- unpack: lane t of a row takes 32 dims (8-bit codes: two pieces of 16, half a row apart,
@@ -760,7 +772,8 @@ cache_prefix_kernel(const Prefix a) {
             const uint64_t vd = v_desc + b * (kTile / 16);
 #pragma unroll
             for (int kk = 0; kk < kTok / 16; ++kk)
-              tc_mma_f16_ts(tm_o(i), tm_s(i) + kk * 8, vd + kk * (2048 / 16), id_pv,
+              tc_mma_f16_ts(tm_o(i), tm_s(i) + (kk >> 2) * 64 + (kk & 3) * 8, vd + kk * (2048 / 16),
+                            id_pv,
                             (r | kk) ? 1u : 0u);
             tc_commit(&pv_done[i]);
             if (!w.two || i == 1) tc_commit(&v_empty[b]);
