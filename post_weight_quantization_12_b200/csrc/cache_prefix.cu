@@ -19,7 +19,7 @@
 //                    scheduler lets it go first, and every other role waits for it)
 //   warps 4-11, 12-19  softmax of row tile 0 and 1, two threads a row: each takes half of the
 //                    tokens, and half of the dimensions when they bring Q in and write the results
-//   warps 20-23      unpack K and V of the next tiles into two buffers each, loads a tile ahead
+//   warps 20-23, 24-27  unpack K and V of the next tiles into two buffers each, loads a tile ahead
 // With no more than 128 rows in an item, both softmax groups take the same rows and every other
 // token tile. The runs' results (row, fp32, with its log-sum) are joined by cache_merge_kernel.
 #include <cuda_runtime.h>
@@ -33,11 +33,11 @@ namespace {
 
 constexpr int kTok = 128;                  // tokens of a tile
 constexpr int kSm0 = 4;                    // the first softmax warp
-constexpr int kDq0 = 20, kDqWarps = 4;     // the unpacking warps
+constexpr int kDq0 = 20, kDqWarps = 4;     // the unpacking warps of K; those of V follow
 constexpr int kDqRows = kTok / kDqWarps;   // rows of a tile that one of them takes: one a lane
 static_assert(kDqRows == 32, "a lane a row");
 constexpr int kMmaWarp = 0;
-constexpr int kThreads = 32 * (kDq0 + kDqWarps);
+constexpr int kThreads = 32 * (kDq0 + 2 * kDqWarps);
 constexpr float kNegInf = -INFINITY;
 
 struct Prefix {
@@ -208,7 +208,7 @@ cache_prefix_kernel(const Prefix a) {
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], mma_done;
   __shared__ __align__(16) uint32_t valid[4][4];   // of step s in slot s % 4: tokens that count
   __shared__ int k_exp[4], v_exp[4];               // ... and the exponents of its images
-  __shared__ uint32_t warp_top[2][kDqWarps][2];
+  __shared__ uint32_t warp_top[2][2][kDqWarps][2];   // of the unpackers of K and V
   __shared__ float row_x[2][128];                  // of (row tile, row): what its halves exchange
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_flag;
@@ -474,7 +474,10 @@ cache_prefix_kernel(const Prefix a) {
     constexpr int LPR = D / 32, RPI = 32 / LPR;                // lanes a row, rows an access
     constexpr int KI = kDqRows / RPI;
     constexpr int kVec = BITS == 4 ? 1 : 2;                    // 16-byte loads of a lane's codes
-    const int dw = warp - kDq0, t = lane % LPR, g = lane / LPR;
+    // h: 0 unpacks K, 1 unpacks V; each group keeps its own count of steps
+    const int h = warp >= kDq0 + kDqWarps, dw = warp - kDq0 - h * kDqWarps;
+    const int t = lane % LPR, g = lane / LPR;
+    const CacheHalf half = h ? a.cache.half[1] : a.cache.half[0];
     // first dim of piece v of this lane
     auto dim_of = [&](int v) { return BITS == 4 ? 32 * t : 16 * t + v * (D / 2); };
     constexpr int kS = (G + 1) / 2;      // words of a row's scales
@@ -516,9 +519,9 @@ cache_prefix_kernel(const Prefix a) {
       return -1;
     };
     // codes on their way to the slots: each lane copies what it will unpack
-    auto copy_codes = [&](int64_t row, int b, int h) {
+    auto copy_codes = [&](int64_t row, int b) {
       uint8_t* dst = code_slot(b, h) + dw * (SM::kCodeBytes / kDqWarps) + lane * 16;
-      const uint8_t* base = a.cache.half[h].codes + 16 * t;
+      const uint8_t* base = half.codes + 16 * t;
       const int64_t from = max(row, static_cast<int64_t>(0));
 #pragma unroll
       for (int k = 0; k < KI; ++k) {
@@ -528,27 +531,37 @@ cache_prefix_kernel(const Prefix a) {
       }
       cp_commit();
     };
-    // scales (bf16 pairs) and zeros (bytes) of the warp's row `lane` of K and V
-    uint32_t sc[2][kS], zr[2];
+    // scales (bf16 pairs) and zeros (bytes) of the warp's row `lane`; the unpackers of K take V's
+    // scales too: the softmax groups need both exponents with S
+    uint32_t sc[kS], sv[kS], zr;
+    auto load_scales = [&](const uint16_t* s, uint32_t (&x)[kS]) {
+      if constexpr (G == 1) {
+        x[0] = __ldg(s);
+      } else if constexpr (G == 2) {
+        x[0] = __ldg(reinterpret_cast<const uint32_t*>(s));
+      } else {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(s));
+        x[0] = v.x;
+        x[kS - 1] = v.y;
+      }
+    };
     auto load_grids = [&](int64_t row) {
       const int64_t from = max(row, static_cast<int64_t>(0)) * G;
+      load_scales(half.scales + from, sc);
+      if (h == 0) load_scales(a.cache.half[1].scales + from, sv);
+      const uint8_t* z = half.zeros + from;
+      if constexpr (G == 1) zr = __ldg(z);
+      else if constexpr (G == 2) zr = __ldg(reinterpret_cast<const uint16_t*>(z));
+      else zr = __ldg(reinterpret_cast<const uint32_t*>(z));
+    };
+    auto top_of = [&](const uint32_t (&x)[kS]) -> uint32_t {
+      uint32_t top = 0;              // largest scale, as bits; not the ones that are not finite
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint16_t* s = a.cache.half[h].scales + from;
-        const uint8_t* z = a.cache.half[h].zeros + from;
-        if constexpr (G == 1) {
-          sc[h][0] = __ldg(s);
-          zr[h] = __ldg(z);
-        } else if constexpr (G == 2) {
-          sc[h][0] = __ldg(reinterpret_cast<const uint32_t*>(s));
-          zr[h] = __ldg(reinterpret_cast<const uint16_t*>(z));
-        } else {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(s));
-          sc[h][0] = v.x;
-          sc[h][kS - 1] = v.y;
-          zr[h] = __ldg(reinterpret_cast<const uint32_t*>(z));
-        }
+      for (int k = 0; k < G; ++k) {
+        const uint32_t y = k & 1 ? x[k / 2] >> 16 : x[k / 2] & 0xFFFFu;
+        top = max(top, y < 0x7F80u ? y : 0u);
       }
+      return __reduce_max_sync(0xffffffffu, top);
     };
     bool ok = true;
     uint32_t gs = 0;
@@ -561,8 +574,7 @@ cache_prefix_kernel(const Prefix a) {
       look(ahead);
       next(ahead);
       rows[k] = resolve();
-      copy_codes(rows[k], k, 0);
-      copy_codes(rows[k], k, 1);
+      copy_codes(rows[k], k);
     }
     look(ahead);
     next(ahead);
@@ -578,72 +590,51 @@ cache_prefix_kernel(const Prefix a) {
       // a token that does not count: zero scales, so its images are zeros
       if (!counts) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int k = 0; k < kS; ++k) sc[h][k] = 0;
+        for (int k = 0; k < kS; ++k) sc[k] = sv[k] = 0;
       }
-      // the tile's largest scales (as bits; not the ones that are not finite)
-      uint32_t top[2] = {0, 0};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int k = 0; k < G; ++k) {
-          const uint32_t x = k & 1 ? sc[h][k / 2] >> 16 : sc[h][k / 2] & 0xFFFFu;
-          top[h] = max(top[h], x < 0x7F80u ? x : 0u);
-        }
-        top[h] = __reduce_max_sync(0xffffffffu, top[h]);
-      }
+      // the tile's largest scales
+      const uint32_t top_own = top_of(sc), top_v = h == 0 ? top_of(sv) : top_own;
       if (lane == 0) {
-        warp_top[gs & 1][dw][0] = top[0];
-        warp_top[gs & 1][dw][1] = top[1];
+        warp_top[h][gs & 1][dw][0] = top_own;
+        warp_top[h][gs & 1][dw][1] = top_v;
       }
       // all the warps leave together if one of them gave up
-      if (named_barrier_or(1, 32 * kDqWarps, !ok)) break;
+      if (named_barrier_or(h == 0 ? 1 : 10, 32 * kDqWarps, !ok)) break;
+      uint32_t top[2] = {0, 0};
 #pragma unroll
       for (int x = 0; x < kDqWarps; ++x) {
-        top[0] = max(top[0], warp_top[gs & 1][x][0]);
-        top[1] = max(top[1], warp_top[gs & 1][x][1]);
+        top[0] = max(top[0], warp_top[h][gs & 1][x][0]);
+        top[1] = max(top[1], warp_top[h][gs & 1][x][1]);
       }
-      int e[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) e[h] = max(static_cast<int>(top[h] >> 7) - 127, -107);
-      v_ref = max(v_ref, e[1]);
-      e[1] = v_ref;
+      v_ref = max(v_ref, max(static_cast<int>(top[1] >> 7) - 127, -107));
+      const int e = h == 0 ? max(static_cast<int>(top[0] >> 7) - 127, -107) : v_ref;
       // this step's grids move on to make room for the next one's
-      uint32_t s_now[2][kS], z_now[2];
+      uint32_t s_h[kS];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        z_now[h] = zr[h];
-#pragma unroll
-        for (int k = 0; k < kS; ++k) s_now[h][k] = sc[h][k];
-      }
+      for (int k = 0; k < kS; ++k) s_h[k] = sc[k];
+      const uint32_t z_h = zr;
       const uint32_t counting = __ballot_sync(0xffffffffu, counts);
       next(now);
       rows[SM::kAhead] = resolve();
       look(ahead);
       next(ahead);
       load_grids(rows[1]);
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        cp_wait<2 * SM::kAhead - 1>();
+      {
+        cp_wait<SM::kAhead - 1>();
         __syncwarp();
         if (ok) ok = mbar_wait_bounded(h == 0 ? &k_empty[b] : &v_empty[b], ph ^ 1u, &abort_flag,
                                        info);
         if (h == 0) {
-          // slot s % 4 was last read by step s - 4's softmax, which PV(s - 4) followed
+          // slot s % 4 was last read by step s - 4's softmax; k_empty of step s - 2 is past it
           if (lane == 0) valid[slot][dw] = counting;
-          if (threadIdx.x == 32 * kDq0) {
-            k_exp[slot] = e[0] - kTop;
-            v_exp[slot] = e[1] - kTop;
+          if (dw == 0 && lane == 0) {
+            k_exp[slot] = e - kTop;
+            v_exp[slot] = v_ref - kTop;
           }
         }
-        const float unit = pow2(max(kTop - (h == 0 ? e[0] : e[1]), -126));
+        const float unit = pow2(max(kTop - e, -126));
         const uint8_t* src = code_slot(cb, h) + dw * (SM::kCodeBytes / kDqWarps) + lane * 16;
         uint8_t* tile = h == 0 ? k_tile(b) : v_tile(b);
-        uint32_t s_h[kS];
-#pragma unroll
-        for (int k = 0; k < kS; ++k) s_h[k] = h == 0 ? s_now[0][k] : s_now[1][k];
-        const uint32_t z_h = h == 0 ? z_now[0] : z_now[1];
 #pragma unroll
         for (int k = 0; k < KI; ++k) {
           const int rl = k * RPI + g, row = dw * kDqRows + rl;
@@ -702,7 +693,7 @@ cache_prefix_kernel(const Prefix a) {
         fence_proxy_async_smem();
         mbar_arrive(h == 0 ? &k_full[b] : &v_full[b]);
         // the slot is free (its lane has read it): the codes of a step to come
-        copy_codes(rows[SM::kAhead], cb, h);
+        copy_codes(rows[SM::kAhead], cb);
       }
 #pragma unroll
       for (int k = 0; k < SM::kAhead; ++k) rows[k] = rows[k + 1];
