@@ -37,6 +37,17 @@ __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
   return d;
 }
 
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // Eight consecutive values of a row.
 template <bool kBf16>
 struct Eight {
@@ -345,6 +356,23 @@ cache_read_kernel(const CacheView c, const CacheRows rows, void* __restrict__ K_
         uint8_t* out = static_cast<uint8_t*>(h == 0 ? K_out : V_out);
         const int head = head0 + u * kPer;
         if (out == nullptr || head >= c.heads) continue;
+        uint8_t* dst = out + ((walk.tok * c.heads + head) * kDim + 8 * l) * kElem;
+        if constexpr (kBits == 4 && kYBf16) {
+          // two at a time: 128 + code and 128 + z are bf16 numbers, their difference is exact, and
+          // its product with the scale is rounded once, as that of fp32 numbers rounded to bf16
+          // would be (8 times 4 bits are exact there)
+          const uint32_t s2 = s[u][h] * 0x00010001u, z2 = (0x4300u + z[u][h]) * 0x00010001u;
+          uint32_t v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)       // values i and i + 4
+            v[i] = mul_bf16x2(
+                sub_bf16x2(((w[u][h][0] >> (4 * i)) & 0x000F000Fu) | 0x43004300u, z2), s2);
+          uint4 y = make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                               __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+          if (walk.page < 0) y = make_uint4(0, 0, 0, 0);
+          __stcs(reinterpret_cast<uint4*>(dst), y);
+          continue;
+        }
         const float sf = bf16_bits_to_float(s[u][h]);
         const float zf = __uint_as_float(0x4B000000u | z[u][h]);     // 2^23 + z
         float y[8];
@@ -358,7 +386,7 @@ cache_read_kernel(const CacheView c, const CacheRows rows, void* __restrict__ K_
 #pragma unroll
           for (int i = 0; i < 8; ++i) y[i] = 0.f;
         }
-        store8<kYBf16>(out + ((walk.tok * c.heads + head) * kDim + 8 * l) * kElem, y);
+        store8<kYBf16>(dst, y);
       }
   }
 }

@@ -310,8 +310,11 @@ __device__ __forceinline__ void weigh(float (&p)[NT][4], float (&m)[NT][2], floa
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (kEdge && !on[nt][e]) p[nt][e] = kNegInf;
-      above |= p[nt][e] > m[nt][e & 1] + 8.f;
     }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) above |= fmaxf(p[nt][k], p[nt][2 + k]) > m[nt][k] + 8.f;
   if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -417,6 +420,8 @@ cache_attend_kernel(const Level a) {
       v_at[h] = C::kK + r * RB + ((byte / 16) ^ swizzle<RB>(r)) * 16 + byte % 16;
     }
   }
+  // slots 2t and 2t + 1 are tokens 2t and 2t + 1, or the other way round
+  const uint32_t z_order = t & 1 ? 0x4041u : 0x4140u;
   // scales and zeros of the 16 tokens: 6 G pieces of 16 bytes, a lane a piece
   const bool grid_lane = lane < 6 * G;
   const uint8_t* g_src;
@@ -745,8 +750,10 @@ cache_attend_kernel(const Level a) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint8_t* z = zvp + (2 * t + 8 * h) * G + gr;       // tokens 2t and 2t + 1
-          const uint32_t z0 = z[0], z1 = z[G];
-          zp[h] = (t & 1 ? z1 | z0 << 16 : z0 | z1 << 16) | 0x80008000u;
+          uint32_t zz;
+          if constexpr (G == 1) zz = *reinterpret_cast<const uint16_t*>(z);
+          else zz = z[0] | static_cast<uint32_t>(z[G]) << 8;
+          zp[h] = __byte_perm(zz, 0x80808080u, z_order);           // 0x80 above each: minus z
         }
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
