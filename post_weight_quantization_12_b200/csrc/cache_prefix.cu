@@ -239,7 +239,9 @@ cache_prefix_kernel(const Prefix a) {
   const uint32_t tmem = tmem_base_sh;
   auto tm_s = [&](int i) { return tmem + 128 * i; };   // S; P over the first half of each half
   auto tm_o = [&](int i) { return tmem + 256 + D * i; };
-  griddep_wait();
+  // What this kernel reads (queries, cache) was complete before the kernel in front of it, which
+  // waited for it, let this one start; the results of that kernel are not read here. So the wait for
+  // it comes at the end, where it keeps the order for the kernel that follows.
   griddep_launch_dependents();
   int32_t* info = a.info;
 
@@ -792,6 +794,7 @@ cache_prefix_kernel(const Prefix a) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  griddep_wait();
 }
 
 // out = the results of the prefix's runs and, where a row met own positions, of its own level,
