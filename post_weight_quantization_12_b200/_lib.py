@@ -293,13 +293,14 @@ def cache_rows(n, table, lengths, starts):
 
 
 def _heads_ld(t, name, heads, dim):
-    """Row stride of a [n, heads, dim] tensor whose rows are dense."""
+    """Row stride of a [n, heads, dim] tensor whose rows are dense (of one row: its width, whatever
+    the tensor was cut from)."""
     shape, strides = t.shape, t.stride()
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"{name} must be [n, {heads}, {dim}]")
     if strides[2] != 1 or (heads > 1 and strides[1] != dim):
         raise ValueError(f"{name} must hold the heads of a row one after another")
-    return strides[0] if shape[0] > 1 else max(strides[0], heads * dim)
+    return strides[0] if shape[0] > 1 else heads * dim
 
 
 def _same_rows(t, like, name):

@@ -190,3 +190,12 @@ def test_structs_match_the_header():
                 fields += [re.findall(r"(\w+)$", f.strip())[0] for f in [first, *rest]]
         assert [f.replace("_dev", "") for f in fields] == [f for f, _ in struct._fields_]
     assert ctypes.sizeof(_lib.Cache) == 6 * 8 + 8 + 5 * 4 + 4
+
+
+def test_one_row_has_the_stride_of_its_width():
+    """A single row cut from any tensor: its row stride says nothing and is not passed on."""
+    base = torch.zeros(7 * 300 + 1, dtype=torch.bfloat16)
+    for stride in (1, 256, 301, 2048):
+        x = base.as_strided((1, 2, 128), (stride, 128, 1))
+        assert _lib._heads_ld(x, "x", 2, 128) == 256
+    assert _lib._heads_ld(base.as_strided((3, 2, 128), (264, 128, 1)), "x", 2, 128) == 264

@@ -498,3 +498,150 @@ def test_an_item_per_warp():
     _run(host, lengths, news, 2, rows={0, 1, 6, 7, 60, 62, 100, 126})
     news = np.minimum(rng.integers(1, 4, batch), 3)
     _run(host, lengths, news, 2, rows={0, 1, 2, 14, 15, 100, 200})
+
+
+# ------------------------------------------------------------------------------------------------
+# calls at once, captured, replayed
+# ------------------------------------------------------------------------------------------------
+def _shared_call(seed, batch=40):
+    """A cache and the arguments of a call over a prefix of up to 704 positions, met by more than 32
+    rows."""
+    host = HostCache(44 + 4 * batch, 2, 16, 128, 4, 64, seed=seed)
+    lengths = ((np.arange(batch) * 11) % 50 + 1).astype(np.int32)
+    ptable = np.random.default_rng(seed).permutation(44).astype(np.int32)
+    table = make_table(lengths, 16, 44 + 4 * batch, seed, first=44)
+    return host, ptable, table, lengths, _q(batch, 8, 128, seed)
+
+
+def test_shared_calls_at_once_and_behind_one_another():
+    """Calls on two streams at once, several behind one another on each, every one with a workspace
+    of its own: each result is the one of a call alone. Tables of one page leave the sequences' own
+    level one kernel, without a join in front of the prefix's."""
+    calls = []
+    for seed, batch, prefix in ((61, 40, 700), (62, 100, 130), (63, 33, 650)):
+        host, ptable, table, lengths, q = _shared_call(seed, batch)
+        if seed == 63:
+            lengths, table = np.ones_like(lengths), table[:, :1].copy()
+        cache = host.device()
+        args = (q.to(DEV), dev(ptable), prefix, dev(table), dev(lengths))
+        alone = cache.attend_shared(*args)
+        torch.cuda.synchronize()
+        check_attend(alone, host, table, lengths, np.arange(batch + 1), q, 128 ** -0.5,
+                     prefix=(ptable, prefix), image16=True, rows={0, batch // 2, batch - 1})
+        calls.append((cache, args, alone))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for k in range(4):
+        for s in streams:
+            for cache, args, alone in calls if s is streams[k % 2] else reversed(calls):
+                outs.append((cache.attend_shared(*args, stream=s), alone))
+    torch.cuda.synchronize()
+    for out, alone in outs:
+        assert torch.equal(out, alone)
+
+
+def test_shared_step_replayed_with_new_queries_and_lengths():
+    """append + attend_shared captured once; each replay equals the same calls made eagerly."""
+    host, ptable, table, lengths, q = _shared_call(64)
+    batch = len(lengths)
+    caches = [host.device() for _ in range(2)]
+    pt, t = dev(ptable), dev(np.where(table < 0, 0, table).astype(np.int32))
+    n = dev(np.ones(batch, np.int32))
+    kv = torch.zeros(batch, 2, 128, dtype=torch.bfloat16, device=DEV)
+    qd = q.to(DEV)
+    # each sequence on its first page only: 16 positions of its own
+    t = t[:, :1].contiguous()
+
+    def step(cache):
+        cache.append(kv, kv, t, n)
+        return cache.attend_shared(qd, pt, 700, t, n)
+    step(caches[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(caches[0])
+    g = torch.Generator().manual_seed(4)
+    for length in (1, 2, 9, 16):
+        kv.copy_(torch.randn(batch, 2, 128, generator=g))
+        qd.copy_(torch.randn(batch, 8, 128, generator=g))
+        n.fill_(length)
+        for _ in range(2):                # the same step twice over: same codes, same result
+            graph.replay()
+        want = step(caches[1])
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert torch.equal(caches[0].k_codes, caches[1].k_codes)
+    assert int(caches[0].info.item()) == 0 and int(caches[1].info.item()) == 0
+
+
+def test_first_calls_of_a_process_under_capture():
+    """Nothing has to run before a capture: a fresh process captures every call as its first."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from post_weight_quantization_12_b200 import api
+dev = "cuda"
+cache = api.QuantizedCache(64, 2, 128, 16, 4)
+i32 = dict(dtype=torch.int32, device=dev)
+table, lengths = torch.arange(20, 60, **i32)[:, None], torch.ones(40, **i32)
+pt, starts = torch.arange(20, **i32), torch.tensor([0, 300], **i32)
+x = torch.randn(40, 2, 128, device=dev).bfloat16()
+pre = torch.randn(300, 2, 128, device=dev).bfloat16()
+plen = torch.tensor([300], **i32)
+q = torch.randn(40, 8, 128, device=dev).bfloat16()
+torch.cuda.synchronize()
+def step():
+    cache.append(pre, pre, pt[None], plen, starts)
+    cache.append(x, x, table, lengths)
+    return (cache.attend(q, table, lengths), cache.attend_shared(q, pt, 300, table, lengths),
+            cache.attend_shared(q[:4], pt, 300, table[:4], lengths[:4]), *cache.read(table, lengths))
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = step()
+graph.replay()
+torch.cuda.synchronize()
+eager = step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(captured, eager))
+assert torch.isfinite(eager[1]).all() and int(cache.info.item()) == 0
+print("as eager")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "as eager" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_shared_queries_that_are_not_finite_stay_in_their_row(bad):
+    host, ptable, table, lengths, q = _shared_call(65)
+    cache = host.device()
+    args = (dev(ptable), 700, dev(table), dev(lengths))
+    clean = cache.attend_shared(q.to(DEV), *args)
+    q[3, 5, 17] = bad
+    out = cache.attend_shared(q.to(DEV), *args)
+    own = cache.attend(q.to(DEV), *args[2:])
+    torch.cuda.synchronize()
+    if math.isnan(bad):
+        assert torch.isnan(out[3, 5]).all()
+    clean[3, 5], out[3, 5] = 0, 0
+    assert torch.equal(out, clean)
+    own[3, 5] = 0
+    assert torch.isfinite(own).all()
+
+
+def test_one_row_cut_from_a_wider_tensor():
+    """A single row whose tensor has an odd row stride, for queries, keys and outputs."""
+    host = HostCache(4, 2, 16, 128, 4, 128, seed=66)
+    cache, table, lengths = host.device(), np.array([[2, 1]], np.int32), np.array([20], np.int32)
+    q = _q(1, 4, 128, 67)
+    wide = torch.zeros(4 * 128 + 8, dtype=torch.bfloat16, device=DEV)
+    odd = wide.as_strided((1, 4, 128), (4 * 128 + 3, 128, 1))
+    odd.copy_(q)
+    out = cache.attend(odd, dev(table), dev(lengths))
+    torch.cuda.synchronize()
+    check_attend(out, host, table, lengths, [0, 1], q, 128 ** -0.5)
+    want = cache.attend(q.to(DEV), dev(table), dev(lengths))
+    assert torch.equal(out, want)
