@@ -10,9 +10,17 @@
 // most) keeps both ends of [lo, hi] on the grid. A group with a value that is not finite, or whose
 // step is not, gets a NaN scale and zero codes, so it reads back as NaN.
 //
-// Both kernels move each byte once and are bound by HBM: append reads 2 or 4 bytes a value, writes
-// bits / 8 and, where the caller wants the values back, 2 or 4 more; read writes 2 or 4 for
-// bits / 8 read.
+// Both kernels move each byte once: append reads 2 or 4 bytes a value, writes bits / 8 and, where the
+// caller wants the values back, 2 or 4 more; read writes 2 or 4 for bits / 8 read. What bounds them
+// is HBM for read and, for append, the instructions of the grid beside it. Measured (128 dimensions,
+// 4-bit codes, one grid a row, bf16, 8 heads, page 128; fractions of the measured copy bandwidth):
+//   append of 4 prompts of up to 16,384 tokens with both values back   106 us, 0.70; 69 % of the
+//     issue slots, 735 warp instructions per 1024 values. Three CTAs of 256 threads an SM (80
+//     registers) took 109 us when the others were tried: bounded to four 111, not bounded 125.
+//   read of 16 sequences of up to 8192 tokens  97 us, 0.82. Four CTAs an SM took 100 us when 5, 6
+//     and 8, and four heads a warp instead of two, were tried: 107 to 121.
+// A single step (one token of 16 sequences) is 3.3 us on the device, of a read of 777 tokens 3.0:
+// the launch and one trip to memory.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -423,7 +431,6 @@ gptq_status launch_rows(const CacheView& c, const CacheRows& r, int per_warp, cu
   return launch_pdl(kKernel, row_grid<kKernel>(c, r.n, per_warp), dim3(kRowThreads), 0, stream, c,
                     r, args...);
 }
-
 
 template <int kDim, int kBits, int kGroup>
 gptq_status append_as(const CacheView& c, const CacheRows& r, const void* K, int64_t ldk,

@@ -22,6 +22,17 @@
 //   warps 20-23, 24-27  unpack K and V of the next tiles into two buffers each, loads a tile ahead
 // With no more than 128 rows in an item, both softmax groups take the same rows and every other
 // token tile. The runs' results (row, fp32, with its log-sum) are joined by cache_merge_kernel.
+//
+// What bounds it. Two row tiles: the chain of a step. Both products read operands from shared or
+// tensor memory (about 840 cycles of S, 700 of O a row tile and token tile), and with the hand-overs
+// between them a step of both row tiles takes about 4.4k cycles: 128 sequences x 8 heads of 4-bit
+// codes x 4 query heads, prefix 32,768, 130 us in all, 532 TFLOP/s (0.32 of the measured bf16 rate);
+// this kernel 87 us, tensor pipe 37 % busy. One row tile: unpacking, about 3.0k cycles a token tile:
+// 96 sequences x 32 heads of 8-bit codes, prefix 8192, 122 us in all, this kernel 47 us. The rest
+// of both is the sequences' own level, the merge (about 9 us) and what lies between them.
+// Tried and slower (first case): S in two halves of the tokens (140 to 163 us), the eight unpacking
+// warps on K and V alike (140 to 146 us). Unpackers of K and V apart: 144 to 139 us. Copies of codes
+// by half sectors: 207 us in the second case where whole ones took 140.
 #include <cuda_runtime.h>
 
 #include <algorithm>
