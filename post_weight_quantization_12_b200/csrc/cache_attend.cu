@@ -114,7 +114,8 @@ struct Level {
 
 struct Sequence {
   int row0, end;                // rows row0 .. row0 + count - 1; end: the nominal end
-  int count, len;
+  int count, len;               // len: positions that the page table reaches
+  int row0_pos;                 // position of row row0: by the given length, also past the table
   int row_tiles, tiles_per;     // tiles of one (head, row tile)
   int64_t tiles;                // of the sequence over all heads
 };
@@ -140,10 +141,11 @@ __device__ __forceinline__ Sequence get_sequence(const Level& a, int64_t b) {
     s.len = __ldg(a.rows.lengths + b);
   }
   const int64_t cap = static_cast<int64_t>(a.cache.width) << a.cache.page_shift;
-  if (s.len < 0 || s.len > cap) {
-    if ((threadIdx.x & 31) == 0) record_info(a.info, GPTQ_INFO_BAD_PAGE);
-    s.len = s.len < 0 ? 0 : static_cast<int>(cap);
-  }
+  const bool bad = s.len < 0 || s.len > cap;
+  if (bad && (threadIdx.x & 31) == 0) record_info(a.info, GPTQ_INFO_BAD_PAGE);
+  s.len = max(s.len, 0);
+  s.row0_pos = s.len - (s.end - s.row0);
+  if (s.len > cap) s.len = static_cast<int>(cap);
   s.row_tiles = (s.count * a.ratio + R - 1) / R;
   s.tiles_per = max(s.len / kTile + (s.len % kTile != 0), 1);
   s.tiles = static_cast<int64_t>(s.tiles_per) * s.row_tiles * a.cache.heads;
@@ -456,9 +458,8 @@ cache_attend_kernel(const Level a) {
     auto limit_of = [&](int j) -> int {
       if (j >= n_rows) return 0;
       if (a.fixed_len >= 0) return s.len;
-      return min(max(s.len - s.end + s.row0 + static_cast<int>(static_cast<uint32_t>(j) /
-                                                               static_cast<uint32_t>(a.ratio)) + 1,
-                     0), s.len);
+      return min(max(s.row0_pos + static_cast<int>(static_cast<uint32_t>(j) /
+                                                   static_cast<uint32_t>(a.ratio)) + 1, 0), s.len);
     };
     // (a tile's rows past the last one meet whatever the others do; their results are dropped)
     const int limit_lo = limit_of(row_first);
