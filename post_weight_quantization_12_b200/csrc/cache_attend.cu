@@ -17,9 +17,9 @@
 // points' share is a small part of it.
 // The queries are fp16 after a power-of-two scale per row (bf16's 8 bits fit in fp16's 11; values
 // 2^-38 below the row's largest are lost). The weights w_t s_t become fp16 (rounding 2^-12 of each)
-// relative to their own running maximum: with u_t = x_t + log2(s_t) and M >= max u - 8 the operand
-// is 2^(u_t - M), whatever range the scales have, and the denominator sums 2^(u_t - M) / s_t. Sums,
-// maxima and denominators are fp32.
+// relative to their own running reference: with u_t = x_t + log2(s_t) and M >= max u - 15 the operand
+// is 2^(u_t - M), whatever range the scales have. The denominator has a reference of its own and
+// sums 2^(x_t - m): the scales do not enter it. Sums, references and denominators are fp32.
 //
 // The work is cut evenly: tiles of 64 tokens (16 where a warp works alone) of all (sequence, head,
 // row tile) items are numbered in order and each CTA or warp takes one run of them. A run that
@@ -311,39 +311,58 @@ __device__ __forceinline__ void finish(const Level& a, int64_t tok, int qhead, i
   *reinterpret_cast<uint2*>(a.out + tok * a.ldo + static_cast<int64_t>(qhead) * D + d) = v;
 }
 
-// One step's weights from its products: u = x c + log2(s) per token and row, the running reference
-// M, and 2^(u - M) in p. kEdge: some token does not count for some row (u = -inf there).
+// One step's weights from its scores. x: score per token and row, in powers of two; ls: log2 of a
+// token's reference scale. Two references run along, each kept until a score passes it by far:
+//   m for the denominator: l sums 2^(x - m), up to 2^64 a token (fp32 has the range), and
+//   M for the operand of the product with V: p = 2^(x + ls - M), up to 2^15 a token (fp16 ends at
+//   65504). A new M is set 2^7 below the largest, so that the fp16 numbers' range serves the small.
+// A denominator that summed p over the scale would lose a token whose p is flushed to 0, however
+// much weight its score gives it beside tokens of large scales. kEdge: some token does not count for
+// some row.
+constexpr float kFirst = -3e38f;          // a reference before the first score
 template <int D, int NT, bool kEdge>
-__device__ __forceinline__ void weigh(float (&p)[NT][4], float (&m)[NT][2], float (&l)[NT][2],
-                                      float (&o)[NT][D / 16][4], const float (&rs)[2],
+__device__ __forceinline__ void weigh(const float (&x)[NT][4], const float (&ls)[2],
+                                      float (&p)[NT][4], float (&m)[NT][2], float (&l)[NT][2],
+                                      float (&M)[NT][2], float (&o)[NT][D / 16][4],
                                       const bool (&on)[NT][4]) {
   bool above = false;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (kEdge && !on[nt][e]) p[nt][e] = kNegInf;
-    }
+    for (int e = 0; e < 4; ++e)
+      p[nt][e] = kEdge && !on[nt][e] ? kNegInf : x[nt][e] + ls[e >> 1];
+  auto score = [&](int nt, int e) { return kEdge && !on[nt][e] ? kNegInf : x[nt][e]; };
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int k = 0; k < 2; ++k) above |= fmaxf(p[nt][k], p[nt][2 + k]) > m[nt][k] + 8.f;
+    for (int k = 0; k < 2; ++k) {
+      above |= fmaxf(score(nt, k), score(nt, 2 + k)) > m[nt][k] + 64.f;
+      above |= fmaxf(p[nt][k], p[nt][2 + k]) > M[nt][k] + 15.f;
+    }
   if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float top = fmaxf(m[nt][k], fmaxf(p[nt][k], p[nt][2 + k]));
+        float top = fmaxf(score(nt, k), score(nt, 2 + k)), top_p = fmaxf(p[nt][k], p[nt][2 + k]);
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1)
+        for (int off = 4; off < 32; off <<= 1) {
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        const float f = m[nt][k] == kNegInf ? 0.f : ex2(m[nt][k] - top);
-        m[nt][k] = top;
-        l[nt][k] *= f;
+          top_p = fmaxf(top_p, __shfl_xor_sync(0xffffffffu, top_p, off));
+        }
+        // only of the rows that need it: a row's result does not depend on the others'
+        if (top > m[nt][k] + 64.f) {
+          l[nt][k] *= ex2(m[nt][k] - top);
+          m[nt][k] = top;
+        }
+        if (top_p > M[nt][k] + 15.f) {
+          const float f = ex2(M[nt][k] - (top_p - 7.f));
+          M[nt][k] = top_p - 7.f;
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d) {
-          o[nt][d][k] *= f;
-          o[nt][d][2 + k] *= f;
+          for (int d = 0; d < D / 16; ++d) {
+            o[nt][d][k] *= f;
+            o[nt][d][2 + k] *= f;
+          }
         }
       }
   }
@@ -351,11 +370,10 @@ __device__ __forceinline__ void weigh(float (&p)[NT][4], float (&m)[NT][2], floa
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float ref = m[nt][e & 1];
-      const float w = ex2(p[nt][e] - (kEdge && ref == kNegInf ? 0.f : ref));
       // a token that does not count may have any grid (NaN too): out by selection
-      p[nt][e] = kEdge && !on[nt][e] ? 0.f : w;
-      l[nt][e & 1] = kEdge && !on[nt][e] ? l[nt][e & 1] : fmaf(w, rs[e >> 1], l[nt][e & 1]);
+      const bool counts = !kEdge || on[nt][e];
+      p[nt][e] = counts ? ex2(p[nt][e] - M[nt][e & 1]) : 0.f;
+      l[nt][e & 1] += counts ? ex2(x[nt][e] - m[nt][e & 1]) : 0.f;
     }
 }
 
@@ -366,7 +384,7 @@ cache_attend_kernel(const Level a) {
   constexpr int G = C::G, R = C::R, RB = C::RB, kTile = C::kTile;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Find find;
-  __shared__ float row_m[kWarps][R], row_l[kWarps][R];
+  __shared__ float row_lse[kWarps][R];
   // (the broadcast tells the compiler that the warp's number is the same in all its lanes)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -598,7 +616,7 @@ cache_attend_kernel(const Level a) {
             __shfl_sync(0xffffffffu, down, (2 * t + k) * 4) * 16777216.f * a.scale_log2;
     }
 
-    float o[NT][D / 16][4], m[NT][2], l[NT][2];
+    float o[NT][D / 16][4], m[NT][2], l[NT][2], M[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -607,7 +625,7 @@ cache_attend_kernel(const Level a) {
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        m[nt][k] = kNegInf;
+        m[nt][k] = M[nt][k] = kFirst;
         l[nt][k] = 0.f;
       }
     }
@@ -624,7 +642,7 @@ cache_attend_kernel(const Level a) {
       const int pos = first + i * kTile;
 
       // grids of slots g and g + 8
-      float sk[2][G], nz[2][G], ratio_v[2][G], ls[2], rs[2];
+      float sk[2][G], nz[2][G], ratio_v[2][G], ls[2];
       const uint8_t* grids = st + 2 * C::kK;
       const uint8_t* zvp = grids + 80 * G;
 #pragma unroll
@@ -639,12 +657,11 @@ cache_attend_kernel(const Level a) {
           sv[gr] = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(grids + 48 * G)[at]);
           top = fmaxf(top, sv[gr]);
         }
-        // the token's reference scale (its largest, at least 2^-96 so that sums of 1 / s stay
-        // finite) and each group's share of it
+        // the token's reference scale (its largest, at least 2^-96) and each group's share of it
         ls[h] = lg2(top);
-        rs[h] = rcp(top);
+        const float rs = rcp(top);
 #pragma unroll
-        for (int gr = 0; gr < G; ++gr) ratio_v[h][gr] = sv[gr] * rs[h];
+        for (int gr = 0; gr < G; ++gr) ratio_v[h][gr] = sv[gr] * rs;
       }
 
       // ---- x: 16 tokens x 8 NT rows ----
@@ -706,19 +723,19 @@ cache_attend_kernel(const Level a) {
                                                  c[nt][e] + c2[nt][e]), x[nt][e]);
       }
 
-      // ---- weights relative to the running reference M ----
+      // ---- weights relative to the running references ----
       float p[NT][4];
       bool on[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          p[nt][e] = fmaf(x[nt][e], row_scale[nt][e & 1], ls[e >> 1]);
+          x[nt][e] *= row_scale[nt][e & 1];
           on[nt][e] = true;
         }
       uint32_t bf[NT][G][2];
       if (have && pos + kStep <= limit_lo) {
-        weigh<D, NT, false>(p, m, l, o, rs, on);
+        weigh<D, NT, false>(x, ls, p, m, l, M, o, on);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -734,7 +751,7 @@ cache_attend_kernel(const Level a) {
           for (int e = 0; e < 4; ++e)
             on[nt][e] = have && pos + k_tok + 8 * (e >> 1) <
                                     limit_of(row_first + nt * 8 + 2 * t + (e & 1));
-        weigh<D, NT, true>(p, m, l, o, rs, on);
+        weigh<D, NT, true>(x, ls, p, m, l, M, o, on);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -817,37 +834,35 @@ cache_attend_kernel(const Level a) {
     }
     cp_wait<0>();
 
-    // ---- join the four warps ----
+    // ---- join the worker's warps ----
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
+        for (int off = 4; off < 32; off <<= 1)
           l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], off);
-        }
     worker_sync();         // the rings are idle
+    // each warp's own results, divided by their weights (so in the range of the values), and the
+    // logarithm of the weights' sum
     float* res = reinterpret_cast<float*>(ring);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (g == 0) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int r = nt * 8 + 2 * t + k;
-          row_m[warp][r] = m[nt][k];
-          row_l[warp][r] = l[nt][k];
+      for (int k = 0; k < 2; ++k) {
+        const int r = nt * 8 + 2 * t + k;
+        if (g == 0) row_lse[warp][r] = l[nt][k] == 0.f ? kNegInf : m[nt][k] + log2f(l[nt][k]);
+        const float inv = l[nt][k] == 0.f ? 0.f : 16777216.f / l[nt][k];
+        // 2^(M - m) as a square: M and m may lie further apart than one factor reaches
+        const float f = ex2(0.5f * (M[nt][k] - m[nt][k]));
+#pragma unroll
+        for (int tile = 0; tile < D / 16; ++tile) {
+          const int gr = tile / (GROUP / 16), i = tile % (GROUP / 16);
+          const int d = gr * GROUP + g * (GROUP / 8) + 2 * i;
+          *reinterpret_cast<float2*>(res + r * C::kPad + d) =
+              make_float2(o[nt][tile][k] * inv * f * f, o[nt][tile][2 + k] * inv * f * f);
         }
       }
-#pragma unroll
-      for (int tile = 0; tile < D / 16; ++tile) {
-        const int gr = tile / (GROUP / 16), i = tile % (GROUP / 16);
-        const int d = gr * GROUP + g * (GROUP / 8) + 2 * i;
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          *reinterpret_cast<float2*>(res + (nt * 8 + 2 * t + k) * C::kPad + d) =
-              make_float2(o[nt][tile][k] * 16777216.f, o[nt][tile][2 + k] * 16777216.f);
-      }
-    }
     worker_sync();
     const bool whole = run == s.tiles_per;
     const int64_t slot = tile0 == 0 ? 2 * me + 1 : 2 * me;
@@ -856,27 +871,34 @@ cache_attend_kernel(const Level a) {
       const int r = k / (D / 4), d = k % (D / 4) * 4;
       const int j = row_first + r;
       if (j >= n_rows) continue;
-      float top = kNegInf;
+      float4 acc;
+      float lse;
+      if constexpr (WPI == 1) {
+        acc = *reinterpret_cast<const float4*>(res + r * C::kPad + d);
+        lse = row_lse[warp][r];
+      } else {
+        float top = kNegInf;
 #pragma unroll
-      for (int w = 0; w < WPI; ++w) top = fmaxf(top, row_m[w0 + w][r]);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      float den = 0.f;
+        for (int w = 0; w < WPI; ++w) top = fmaxf(top, row_lse[w0 + w][r]);
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float den = 0.f;
 #pragma unroll
-      for (int w = 0; w < WPI; ++w) {
-        const float mw = row_m[w0 + w][r], lw = row_l[w0 + w][r];
-        // a warp without a finite maximum met nothing, or only NaN (its sum is then NaN)
-        const float f = mw == kNegInf ? (lw == 0.f ? 0.f : 1.f) : ex2(mw - top);
-        const float4 v = *reinterpret_cast<const float4*>(
-            reinterpret_cast<const float*>(smem + (w0 + w) * C::kRing) + r * C::kPad + d);
-        den = fmaf(f, lw, den);
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
+        for (int w = 0; w < WPI; ++w) {
+          // a warp that met nothing counts for nothing; one that met NaN has NaN weights
+          const float lw = row_lse[w0 + w][r];
+          const float f = lw == kNegInf ? 0.f : ex2(lw - (top == kNegInf ? 0.f : top));
+          const float4 v = *reinterpret_cast<const float4*>(
+              reinterpret_cast<const float*>(smem + (w0 + w) * C::kRing) + r * C::kPad + d);
+          den += f;
+          acc.x = fmaf(f, v.x, acc.x);
+          acc.y = fmaf(f, v.y, acc.y);
+          acc.z = fmaf(f, v.z, acc.z);
+          acc.w = fmaf(f, v.w, acc.w);
+        }
+        const float inv = den == 0.f ? 0.f : 1.f / den;
+        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        lse = den == 0.f ? kNegInf : (top == kNegInf ? 0.f : top) + log2f(den);
       }
-      const float inv = den == 0.f ? 0.f : 1.f / den;
-      acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-      const float lse = den == 0.f ? kNegInf : (top == kNegInf ? 0.f : top) + log2f(den);
       if (whole) {
         const uint32_t tk = static_cast<uint32_t>(j) / static_cast<uint32_t>(a.ratio);
         finish<D>(a, s.row0 + static_cast<int64_t>(tk),

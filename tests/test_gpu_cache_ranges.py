@@ -1,15 +1,87 @@
-"""Attention over caches whose lengths, queries or grids leave the usual range: every legal finite
+"""Attention over caches whose grids, queries or lengths leave the usual range: every legal finite
 input is within the bound of oracle.attend_bound."""
 import numpy as np
 import pytest
 import torch
 
+import oracle
 from cache_util import DEV, HostCache, check_attend, dev
 from post_weight_quantization_12_b200 import _lib
 
 pytestmark = pytest.mark.gpu
 
 
+def _host(k, v, bits, group, page=16):
+    """A cache of one head whose slots hold k and v [tokens, dim], page after page."""
+    host = HostCache.__new__(HostCache)
+    host.bits, host.dim, host.page, host.heads = bits, k.shape[1], page, 1
+    pages = -(-k.shape[0] // page)
+    host.part = {}
+    for half, x in (("k", k), ("v", v)):
+        full = np.zeros((pages * page, k.shape[1]), np.float32)
+        full[:len(x)] = x
+        host.part[half] = oracle.grid_quantize(full.reshape(pages, 1, page, -1), bits, group)
+    return host
+
+
+def _queries(n, dim, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(n, 1, dim, generator=g).to(torch.bfloat16)
+
+
+def _attend(host, tokens, q, scale=None, rows=None):
+    """Every row of q [rows, 1, dim] meets the first `tokens` positions: as the query heads of one
+    token, and as a shared prefix."""
+    scale = host.dim ** -0.5 if scale is None else scale
+    pages = host.part["k"][0].shape[0]
+    table = np.arange(pages, dtype=np.int32)
+    n, cache = q.shape[0], host.device()
+    one = q.transpose(0, 1)
+    own = cache.attend(one.contiguous().to(DEV), dev(table[None]),
+                       dev(np.array([tokens], np.int32)), scale=scale)
+    pre = cache.attend_shared(q.to(DEV), dev(table), tokens, dev(np.zeros((n, 1), np.int32)),
+                              dev(np.zeros(n, np.int32)), scale=scale)
+    torch.cuda.synchronize()
+    assert int(cache.info.item()) == 0
+    args = [p[:, 0].reshape(-1, p.shape[-1])[:tokens] for half in "kv" for p in host.part[half]]
+    for i in range(n) if rows is None else rows:
+        for got, shared in ((own[0, i], False), (pre[i, 0], True)):
+            ref, tol = oracle.attend_bound(q[i, 0].double().numpy(), *args, scale)
+            err = np.abs(got.double().cpu().numpy() - ref)
+            assert np.all(err <= tol), (i, shared, float((err / tol).max()), int((err > tol).sum()))
+
+
+FORMATS = [(128, 4, 128), (128, 8, 128), (128, 4, 32), (128, 8, 64), (64, 4, 64), (64, 8, 32)]
+
+
+@pytest.mark.parametrize("dim,bits,group", FORMATS)
+@pytest.mark.parametrize("n", [1, 12])
+@pytest.mark.parametrize("small,large,every", [(-60, 70, 9), (-60, 60, 9), (-90, 90, 5),
+                                               (-80, 60, 150)])
+def test_value_scales_far_apart(dim, bits, group, n, small, large, every):
+    """Even weights: the tokens with the small scales count in the sum of the weights in full, and
+    where there are no large ones among a run's tokens their values do, too."""
+    rng = np.random.default_rng(every)
+    k, v = (rng.standard_normal((150, dim)).astype(np.float32) for _ in range(2))
+    e = np.where(np.arange(150) % every == 4, large, small).astype(np.float32)
+    host = _host(k, v * np.exp2(e)[:, None], bits, group)
+    _attend(host, 150, torch.zeros(n, 1, dim, dtype=torch.bfloat16))
+    _attend(host, 150, _queries(n, dim, 1))
+
+
+@pytest.mark.parametrize("n", [1, 12])
+def test_value_scales_far_apart_in_a_long_sequence(n):
+    """The same over many runs, which are joined."""
+    rng = np.random.default_rng(2)
+    k, v = (rng.standard_normal((9000, 64)).astype(np.float32) for _ in range(2))
+    e = np.where(rng.random(9000) < 0.01, 65.0, -60.0).astype(np.float32)
+    host = _host(k, v * np.exp2(e)[:, None], 8, 64)
+    _attend(host, 9000, torch.zeros(n, 1, 64, dtype=torch.bfloat16))
+
+
+# ------------------------------------------------------------------------------------------------
+# lengths
+# ------------------------------------------------------------------------------------------------
 @pytest.mark.parametrize("news,ratio", [(3, 2), (20, 3)])
 @pytest.mark.parametrize("over", [1, 2, 15, 1000])
 def test_rows_at_positions_past_the_page_table(news, ratio, over):
