@@ -462,11 +462,13 @@ gptq_status gptq_cache_read(const gptq_cache* cache, const gptq_cache_rows* rows
  *   ws_dev          gptq_cache_workspace_size(cache, n, ratio, 0) bytes, 256-byte aligned; calls
  *                   that may overlap on the GPU need one each, graphs captured with the same one
  *                   must not be replayed at the same time.
- * Arithmetic: products of fp16 operands with fp32 sums. Codes are exact; the weights are rounded to
- * fp16 (2^-12 of each, or 2^-25 of the largest), fp32 otherwise; one rounding to bf16 at the end.
- * A token whose V scales all lie below 2^-96 keeps less than fp16's accuracy of them. A NaN scale
- * gives NaN in what meets it: a key's in the row, a value's in its group of dimensions. Results do
- * not depend on timing, and are the same again for the same call on the same device.
+ * Arithmetic: products of fp16 operands with fp32 sums. Codes are exact; a weight with its V scale is
+ * rounded to fp16 (2^-12 of each, or 2^-31 of the largest times the group's largest share of a
+ * token's scales), fp32 otherwise; one rounding to bf16 at the end. Groups of values that are all
+ * zero are left out. The weights' sum does not depend on the scales. A V scale below 2^-126 counts as
+ * 0; scales are not negative. A NaN scale gives NaN in what meets it: a key's in the row, a value's
+ * in its group of dimensions. Results do not depend on timing, and are the same again for the same
+ * call on the same device.
  * n == 0 enqueues nothing. Errors: as gptq_cache_append, GPTQ_EWORKSPACE.
  */
 gptq_status gptq_cache_attend(const gptq_cache* cache, const gptq_cache_rows* rows,

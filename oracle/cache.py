@@ -82,21 +82,32 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float) -> np.ndar
     return (w @ v) / w.sum()
 
 
-def attend_bound(q, kc, ks, kz, vc, vs, vz, scale: float, image16: bool = False):
+def attend_bound(q, kc, ks, kz, vc, vs, vz, scale: float, image16: bool = False,
+                 values16: bool = False, differences: bool = False):
     """One query [dim] over cached tokens: (the result, a bound on the error of a bf16 result of it),
     per dimension, for a kernel with fp32 sums and fp16 operands. The arithmetic written out, nothing
     measured. kc, vc: codes [tokens, dim]; ks, kz, vs, vz: their grids [tokens, groups].
 
     * The sums q . code take dim / 16 + 8 steps, each off by 2^-22 of the magnitudes it adds: x_t
-      moves by (dim / 16 + 8) 2^-22 A_t, A_t = scale sum_groups s (sum |q| code + z sum |q|). The
-      exponential, the logarithm and the products around them add 2^-20. With `image16` the keys are
-      fp16 images of s (code - z), off by 2^-12 each: x_t moves by 2^-12 scale sum |q k| more. A
-      relative error e of the weights moves the result by at most 2 e sum p |v|.
-    * Each weight is rounded to fp16: by 2^-12 of itself, or by 2^-25 of the unit in which the
-      largest is at least 1. With `image16` each value is too, by 2^-12 of itself or 2^-32 of the
-      largest (key images likewise).
+      moves by (dim / 16 + 8) 2^-22 A_t, A_t = scale sum_groups s (sum |q| code + z sum |q|), or
+      with `differences`, where the sums are those of q (code - z), A_t = scale sum |q k|. The score,
+      the largest one, the logarithm of a scale and their differences are fp32 numbers: 2^-22 of
+      their magnitudes. The exponential and the products around it add 2^-20. With `image16` the
+      keys are fp16 images of s (code - z), off by 2^-12 each: x_t moves by 2^-12 scale sum |q k|
+      more. Relative errors e_t of the weights move the result by sum p_t e_t |v_t - out| to first
+      order, the rest being max e of that.
+    * The operand of a token's weight is w s, per group of dimensions, rounded to fp16: by 2^-12 of
+      itself, or by 2^-25 of a unit in which w S times the group's largest s / S is at least 2^6, S
+      being a token's largest scale. A group of a token's values that are all zero does not count.
+      With `image16` each value is an image too, off
+      by 2^-12 of itself or 2^-32 of the largest (key images likewise), and one unit holds for all
+      groups of a token. With `values16` only the values are images, off by 2^-12 of themselves or
+      2^-32 of their token's largest.
     * The sum over tokens runs in steps of 16 and is joined from parts: (tokens / 16 + 64) 2^-22 of
-      sum p |v|.
+      sum p |v|. Each step adds codes and takes zero points out: 2^-22 of sum p s (code + z) more.
+      A code enters as an fp16 subnormal, which the tensor core aligns as if it were 2^-14, that is
+      2^10 codes: each of a step's 16 products is cut at 2^-24 of that and the step's largest
+      weight, 16 * 2^-14 sum over steps of max p s. With `differences` the operands are normal.
     * The result is rounded to bf16: half a step, 2^-8 of the value that is rounded.
     """
     T, dim = kc.shape
@@ -110,18 +121,44 @@ def attend_bound(q, kc, ks, kz, vc, vs, vz, scale: float, image16: bool = False)
     p /= p.sum()
     out, mass = p @ v, p @ np.abs(v)
     aq = np.abs(q).reshape(G, -1)
-    A = scale * (ks.astype(np.float64) *
-                 (np.einsum("tgd,gd->tg", kc.astype(np.float64).reshape(T, G, -1), aq) +
-                  kz * aq.sum(-1))).sum(1)
-    e = (dim / 16 + 8) * 2.0 ** -22 * A.max() + 2.0 ** -20
+    kq = scale * (np.abs(k) @ np.abs(q))
+    if differences:
+        A = kq
+    else:
+        A = scale * (ks.astype(np.float64) *
+                     (np.einsum("tgd,gd->tg", kc.astype(np.float64).reshape(T, G, -1), aq) +
+                      kz * aq.sum(-1))).sum(1)
     steps = (T / 16 + 64) * 2.0 ** -22
+    logs = np.abs(np.log2(vs[vs > 0].astype(np.float64))).max() if (vs > 0).any() else 0.0
+    e = (dim / 16 + 8) * 2.0 ** -22 * A + 2.0 ** -20 + \
+        2.0 ** -22 * (np.abs(x) + np.abs(x.max()) + logs)
     if image16:
-        e += 2.0 ** -12 * scale * (np.abs(k) @ np.abs(q)).max() + \
-            2.0 ** -32 * scale * np.abs(k).max() * np.abs(q).sum()
+        e = (dim / 16 + 8) * 2.0 ** -22 * A.max() + 2.0 ** -20
+        e += 2.0 ** -12 * kq.max() + 2.0 ** -32 * scale * np.abs(k).max() * np.abs(q).sum()
         bound = mass * (2 * e + 2.0 ** -11 + steps) + \
             2.0 ** -25 * p.max() * np.abs(v).sum(0) + 2.0 ** -32 * np.abs(v).max()
     else:
-        unit = (p[:, None] * vs.astype(np.float64)).max()
         z = np.repeat(vz.astype(np.float64), dim // G, 1)
-        bound = mass * (2 * e + 2.0 ** -12 + steps) + 2.0 ** -25 * unit * np.abs(vc - z).sum(0)
+        d = np.abs(vc - z)
+        live_s = np.where(d.reshape(T, G, -1).any(-1), vs.astype(np.float64), 0.0)
+        ps, top_s = p[:, None] * live_s, live_s.max(1)
+        some = top_s > 0
+        share = (live_s[some] / top_s[some, None]).max(0) if some.any() else np.zeros(G)
+        unit = (p * top_s).max() * share                              # per group
+        sums = np.einsum("tg,tgd->gd", ps, (vc + z).reshape(T, G, -1)).reshape(-1)
+        if differences:
+            bound = (p * e) @ np.abs(v - out) * (1 + 2 * (p * e).sum() + e[p > 2.0 ** -20].max())
+        else:
+            bound = 2 * e.max() * mass
+        bound += mass * (2.0 ** -12 + steps) + 2.0 ** -22 * sums
+        if not differences:
+            step = np.pad(ps, ((0, -T % 16), (0, 0))).reshape(-1, 16, G).max(1)
+            bound += 2.0 ** -10 * np.repeat(step.sum(0), dim // G)
+        if values16:
+            top = np.abs(v).max(1)                                    # of a token
+            live = top > 0
+            bound += 2.0 ** -12 * mass + 2.0 ** -32 * (p @ top) + 2.0 ** -31 * (p * top).max() * \
+                (np.abs(v)[live] / top[live, None]).sum(0)
+        else:
+            bound += 2.0 ** -31 * np.repeat(unit, dim // G) * d.sum(0)
     return out, bound + 2.0 ** -8 * (np.abs(out) + bound)

@@ -17,9 +17,11 @@
 // points' share is a small part of it.
 // The queries are fp16 after a power-of-two scale per row (bf16's 8 bits fit in fp16's 11; values
 // 2^-38 below the row's largest are lost). The weights w_t s_t become fp16 (rounding 2^-12 of each)
-// relative to their own running reference: with u_t = x_t + log2(s_t) and M >= max u - 15 the operand
-// is 2^(u_t - M), whatever range the scales have. The denominator has a reference of its own and
-// sums 2^(x_t - m): the scales do not enter it. Sums, references and denominators are fp32.
+// relative to their own running reference, one per group of dimensions: with u_t = x_t + log2(s_t) and
+// M >= max u - 15 the operand is 2^(u_t - M), whatever range the scales have. The denominator has a
+// reference of its own and sums 2^(x_t - m): the scales do not enter it. Sums, references and
+// denominators are fp32. (The tensor core adds at the exponent of its largest operands, and a
+// subnormal counts as 2^-14 there: a step's sums are cut at 2^-14 of a code times its largest weight.)
 //
 // The work is cut evenly: tiles of 64 tokens (16 where a warp works alone) of all (sequence, head,
 // row tile) items are numbered in order and each CTA or warp takes one run of them. A run that
@@ -52,8 +54,10 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStep = 16;                   // tokens of one warp step
 constexpr int kStages = 3;                  // ring depth of a warp, in steps
 constexpr int kMaxResident = 4;             // CTAs per SM
-constexpr float kScaleFloor = 1.2621774e-29f;   // 2^-96, see below
 constexpr float kNegInf = -INFINITY;
+// Scale (bf16 bits) of a group whose values are all zero: 2 / (2^bits - 1), rounded up.
+template <int BITS>
+constexpr uint32_t kEmptyScale = BITS == 4 ? 0x3E09u : 0x3C01u;
 
 // A stage of the ring holds the codes of 16 tokens as they lie in the cache (K, then V, row after
 // row) and their grids. In shared memory the 16-byte chunks of a row are permuted: chunk c of row r
@@ -268,6 +272,13 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// The G scales (bf16, 2 G bytes aligned) of a token, in pairs.
+template <int G>
+__device__ __forceinline__ void load_scales(const uint8_t* p, uint32_t (&x)[(G + 1) / 2]) {
+  if constexpr (G == 1) x[0] = *reinterpret_cast<const uint16_t*>(p);
+  else if constexpr (G == 2) x[0] = *reinterpret_cast<const uint32_t*>(p);
+  else *reinterpret_cast<uint2*>(x) = *reinterpret_cast<const uint2*>(p);
+}
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -311,74 +322,116 @@ __device__ __forceinline__ void finish(const Level& a, int64_t tok, int qhead, i
   *reinterpret_cast<uint2*>(a.out + tok * a.ldo + static_cast<int64_t>(qhead) * D + d) = v;
 }
 
-// One step's weights from its scores. x: score per token and row, in powers of two; ls: log2 of a
-// token's reference scale. Two references run along, each kept until a score passes it by far:
-//   m for the denominator: l sums 2^(x - m), up to 2^64 a token (fp32 has the range), and
-//   M for the operand of the product with V: p = 2^(x + ls - M), up to 2^15 a token (fp16 ends at
-//   65504). A new M is set 2^7 below the largest, so that the fp16 numbers' range serves the small.
-// A denominator that summed p over the scale would lose a token whose p is flushed to 0, however
-// much weight its score gives it beside tokens of large scales. kEdge: some token does not count for
-// some row.
+// The running references of a warp's rows, negated (rows 0 and 1 of each tile side by side):
+//   m: l sums 2^(x - m), up to 2^64 a token (fp32 has the range);
+//   M: a token's weight with its largest scale S is 2^(x + log2 S - M), up to 2^15 (the operand of the
+//      product with V is fp16 and ends at 65504).
+template <int NT>
+struct Refs {
+  float2 m[NT], M[NT];
+};
 constexpr float kFirst = -3e38f;          // a reference before the first score
-template <int D, int NT, bool kEdge>
-__device__ __forceinline__ void weigh(const float (&x)[NT][4], const float (&ls)[2],
-                                      float (&p)[NT][4], float (&m)[NT][2], float (&l)[NT][2],
-                                      float (&M)[NT][2], float (&o)[NT][D / 16][4],
-                                      const bool (&on)[NT][4]) {
-  bool above = false;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      p[nt][e] = kEdge && !on[nt][e] ? kNegInf : x[nt][e] + ls[e >> 1];
-  auto score = [&](int nt, int e) { return kEdge && !on[nt][e] ? kNegInf : x[nt][e]; };
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      above |= fmaxf(score(nt, k), score(nt, 2 + k)) > m[nt][k] + 64.f;
-      above |= fmaxf(p[nt][k], p[nt][2 + k]) > M[nt][k] + 15.f;
-    }
-  if (__any_sync(0xffffffffu, above)) {
+constexpr float kMostBoost = 8.507059e37f;    // 2^126
+
+// One step's weights from its products x (score = x rs, in powers of two, per token and row).
+// ls: log2 of the largest V scale of its two tokens; share: each group's share of it, times the
+// group's power of two. References are kept until a value passes them by far, and then set 2^7 below
+// the largest operand, so that the fp16 numbers' range serves the small ones: they are tried first,
+// and what came out is checked. (A denominator that summed operands over scales would lose a token
+// whose operand is flushed to 0, however much weight its score gives it beside tokens of large
+// scales.) special: the shares need a second look, which `look` takes. kEdge: some token does not
+// count for some row.
+template <int D, int G, int NT, bool kEdge, typename Look>
+__device__ __forceinline__ void weigh(const float (&x)[NT][4], const float (&rs)[NT][2],
+                                      const float (&ls)[2], const float (&share)[2][G],
+                                      uint32_t (&bf)[NT][G][2], Refs<NT>& ref, float (&l)[NT][2],
+                                      float (&o)[NT][D / 16][4], const bool (&on)[NT][4],
+                                      bool special, Look look) {
+  float2 w[NT][2];                        // of token h: rows 0 and 1
+  // true if some operand or weight is beyond what the references allow
+  auto attempt = [&]() -> bool {
+    float most_y = kNegInf, most_z = kNegInf;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float top = fmaxf(score(nt, k), score(nt, 2 + k)), top_p = fmaxf(p[nt][k], p[nt][2 + k]);
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-          top_p = fmaxf(top_p, __shfl_xor_sync(0xffffffffu, top_p, off));
+      for (int h = 0; h < 2; ++h) {
+        const float2 x2 = make_float2(x[nt][2 * h], x[nt][2 * h + 1]);
+        const float2 rs2 = make_float2(rs[nt][0], rs[nt][1]);
+        float2 y = fma2(x2, rs2, ref.m[nt]);
+        float2 z = fma2(x2, rs2, add2(make_float2(ls[h], ls[h]), ref.M[nt]));
+        // a token that does not count may have any grid, NaN too: out by selection
+        const bool on0 = !kEdge || on[nt][2 * h], on1 = !kEdge || on[nt][2 * h + 1];
+        if (kEdge) {
+          y = make_float2(on0 ? y.x : kNegInf, on1 ? y.y : kNegInf);
+          z = make_float2(on0 ? z.x : kNegInf, on1 ? z.y : kNegInf);
         }
-        // only of the rows that need it: a row's result does not depend on the others'
-        if (top > m[nt][k] + 64.f) {
-          l[nt][k] *= ex2(m[nt][k] - top);
-          m[nt][k] = top;
-        }
-        if (top_p > M[nt][k] + 15.f) {
-          const float f = ex2(M[nt][k] - (top_p - 7.f));
-          M[nt][k] = top_p - 7.f;
+        most_y = fmaxf(fmaxf(most_y, y.x), y.y);
+        most_z = fmaxf(fmaxf(most_z, z.x), z.y);
+        w[nt][h] = make_float2(ex2(y.x), ex2(y.y));
+        const float2 p = make_float2(ex2(z.x), ex2(z.y));
 #pragma unroll
-          for (int d = 0; d < D / 16; ++d) {
-            o[nt][d][k] *= f;
-            o[nt][d][2 + k] *= f;
+        for (int gr = 0; gr < G; ++gr) {
+          float2 q = p;
+          if constexpr (G > 1) {
+            q = make_float2(p.x * share[h][gr], p.y * share[h][gr]);
+            if (kEdge) q = make_float2(on0 ? q.x : 0.f, on1 ? q.y : 0.f);
           }
+          bf[nt][gr][h] = half2_bits(q.x, q.y);
         }
       }
+    return most_z > 15.f || most_y > 64.f;
+  };
+  const bool beyond = attempt();
+  if (__any_sync(0xffffffffu, beyond || special)) {
+    look();
+    // only the rows that need a new reference take one: a row's result does not depend on the others'
+    auto renew = [&](int nt, int k, float& m, float& M) {
+      float y[2], z[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        y[h] = kEdge && !on[nt][2 * h + k] ? kNegInf : x[nt][2 * h + k] * rs[nt][k];
+        z[h] = kEdge && !on[nt][2 * h + k] ? kNegInf : y[h] + ls[h];
+      }
+      float top = fmaxf(y[0], y[1]), top_M = fmaxf(z[0], z[1]);
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        top_M = fmaxf(top_M, __shfl_xor_sync(0xffffffffu, top_M, off));
+      }
+      if (top > 64.f - m) {
+        l[nt][k] *= ex2(-m - top);
+        m = -top;
+      }
+      if (top_M > 15.f - M) {
+        const float f = ex2(-M - (top_M - 7.f));
+        M = 7.f - top_M;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          o[nt][d][k] *= f;
+          o[nt][d][2 + k] *= f;
+        }
+      }
+    };
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      renew(nt, 0, ref.m[nt].x, ref.M[nt].x);
+      renew(nt, 1, ref.m[nt].y, ref.M[nt].y);
+    }
+    attempt();
   }
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // a token that does not count may have any grid (NaN too): out by selection
-      const bool counts = !kEdge || on[nt][e];
-      p[nt][e] = counts ? ex2(p[nt][e] - M[nt][e & 1]) : 0.f;
-      l[nt][e & 1] += counts ? ex2(x[nt][e] - m[nt][e & 1]) : 0.f;
-    }
+  for (int nt = 0; nt < NT; ++nt) {
+    const float2 sum = add2(make_float2(l[nt][0], l[nt][1]), add2(w[nt][0], w[nt][1]));
+    l[nt][0] = sum.x;
+    l[nt][1] = sum.y;
+  }
 }
 
+// CTAs an SM: four, but three where a row of 128 dimensions has several grids: their shares and
+// references do not fit in 128 registers (32 sequences of 100 to 16,000 tokens, 8 heads x 4, group 64:
+// 4-bit codes 108 us, and 114 with four; 8-bit codes 123 and 133).
 template <int D, int BITS, int GROUP, int NT, int WPI>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? (D == 128 && GROUP < 128 ? 3 : 4) : 2)
 cache_attend_kernel(const Level a) {
   using C = Cfg<D, BITS, GROUP, NT, WPI>;
   constexpr int G = C::G, R = C::R, RB = C::RB, kTile = C::kTile;
@@ -616,7 +669,12 @@ cache_attend_kernel(const Level a) {
             __shfl_sync(0xffffffffu, down, (2 * t + k) * 4) * 16777216.f * a.scale_log2;
     }
 
-    float o[NT][D / 16][4], m[NT][2], l[NT][2], M[NT][2];
+    float o[NT][D / 16][4], l[NT][2];
+    Refs<NT> ref;
+    // power of two by which each group's shares are taken to at most 1; only where G > 1
+    float boost[G];
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) boost[gr] = kMostBoost;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -625,9 +683,9 @@ cache_attend_kernel(const Level a) {
         for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        m[nt][k] = M[nt][k] = kFirst;
         l[nt][k] = 0.f;
       }
+      ref.m[nt] = ref.M[nt] = make_float2(-kFirst, -kFirst);
     }
 
     uint32_t get = 0;                     // the stage that is consumed
@@ -642,27 +700,105 @@ cache_attend_kernel(const Level a) {
       const int pos = first + i * kTile;
 
       // grids of slots g and g + 8
-      float sk[2][G], nz[2][G], ratio_v[2][G], ls[2];
+      float sk[2][G], nz[2][G];
       const uint8_t* grids = st + 2 * C::kK;
       const uint8_t* zvp = grids + 80 * G;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float top = kScaleFloor;
-        float sv[G];
+        const int r = k_tok + 8 * h;
+        uint32_t k2[(G + 1) / 2], z4;
+        load_scales<G>(grids + 2 * G * r, k2);
+        if constexpr (G == 1) z4 = grids[32 + r];
+        else if constexpr (G == 2) z4 = *reinterpret_cast<const uint16_t*>(grids + 64 + 2 * r);
+        else z4 = *reinterpret_cast<const uint32_t*>(grids + 128 + 4 * r);
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
-          const int at = (k_tok + 8 * h) * G + gr;
-          sk[h][gr] = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(grids)[at]);
-          nz[h][gr] = -static_cast<float>((grids + 32 * G)[at]);
-          sv[gr] = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(grids + 48 * G)[at]);
-          top = fmaxf(top, sv[gr]);
+          sk[h][gr] = __uint_as_float(gr & 1 ? k2[gr / 2] & 0xFFFF0000u : k2[gr / 2] << 16);
+          nz[h][gr] = 8388608.f - __uint_as_float(prmt(z4, 0x4B000000u, 0x7540u | gr));
         }
-        // the token's reference scale (its largest, at least 2^-96) and each group's share of it
-        ls[h] = lg2(top);
-        const float rs = rcp(top);
-#pragma unroll
-        for (int gr = 0; gr < G; ++gr) ratio_v[h][gr] = sv[gr] * rs;
       }
+      // V's: log2 of the token's largest scale, and each group's share of it. The shares of a group
+      // all carry one power of two, which leaves the largest so far at most 1, so the groups of small
+      // values keep their bits. `careful` looks for groups without values: their grid is [-1, 1], a
+      // scale that would push the others' operands out of fp16's range, and zero points times it
+      // leave the rounding of their sum. Their share is 0.
+      float ls[2], share[2][G];
+      bool special = false;
+      auto v_grids = [&](auto careful) {
+        float over = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = k_tok + 8 * h;
+          uint32_t v2[(G + 1) / 2];
+          load_scales<G>(grids + 48 * G + 2 * G * r, v2);
+#pragma unroll
+          for (int gr = 0; gr < G; ++gr) {
+            const uint32_t sv = gr & 1 ? v2[gr / 2] & 0xFFFF0000u : v2[gr / 2] << 16;
+            share[h][gr] = __uint_as_float(sv);
+            if constexpr (!careful.value) {
+              special |= sv == kEmptyScale<BITS> << 16;
+            } else {
+              constexpr int GB = GROUP * BITS / 8;
+              const uint32_t z = zvp[r * G + gr] * (BITS == 4 ? 0x11111111u : 0x01010101u);
+              uint32_t other = 0;
+#pragma unroll
+              for (int i = 0; i < GB / 16; ++i) {          // four lanes to a row
+                const int byte = gr * GB + 16 * i + 4 * t;
+                other |= z ^ *reinterpret_cast<const uint32_t*>(
+                                 st + C::kK + r * RB + ((byte / 16) ^ swizzle<RB>(r)) * 16 +
+                                 byte % 16);
+              }
+              other |= __shfl_xor_sync(0xffffffffu, other, 1);
+              other |= __shfl_xor_sync(0xffffffffu, other, 2);
+              if (other == 0 && sv == kEmptyScale<BITS> << 16) share[h][gr] = 0.f;
+            }
+          }
+          if constexpr (G == 1) {
+            ls[h] = lg2(share[h][0]);
+          } else {
+            float top = 1.1754944e-38f;
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) top = fmaxf(top, share[h][gr]);
+            ls[h] = lg2(top);
+            const float inv = rcp(top);
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+              share[h][gr] = share[h][gr] * inv * boost[gr];
+              over = fmaxf(over, share[h][gr]);
+            }
+          }
+        }
+        special |= over > 1.f;
+      };
+      v_grids(std::false_type{});
+      auto look = [&]() {
+        v_grids(std::true_type{});
+        if constexpr (G > 1) {
+          // only tokens that some row meets: what lies behind them must not matter
+          const bool met0 = have && pos + k_tok < limit_hi, met1 = have && pos + k_tok + 8 < limit_hi;
+#pragma unroll
+          for (int gr = 0; gr < G; ++gr) {
+            float top = fmaxf(met0 ? share[0][gr] : 0.f, met1 ? share[1][gr] : 0.f);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1)
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            if (top > 1.f) {
+              // 2^-e, 2^e the power of two above the largest
+              const uint32_t e = min((__float_as_uint(top) >> 23) + 1u, 253u);
+              const float f = __uint_as_float((254u - e) << 23);
+              boost[gr] *= f;
+              share[0][gr] *= f;
+              share[1][gr] *= f;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int d = gr * (D / G / 16); d < (gr + 1) * (D / G / 16); ++d)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) o[nt][d][i] *= f;
+            }
+          }
+        }
+      };
 
       // ---- x: 16 tokens x 8 NT rows ----
       float x[NT][4];
@@ -724,26 +860,14 @@ cache_attend_kernel(const Level a) {
       }
 
       // ---- weights relative to the running references ----
-      float p[NT][4];
       bool on[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[nt][e] *= row_scale[nt][e & 1];
-          on[nt][e] = true;
-        }
+        for (int e = 0; e < 4; ++e) on[nt][e] = true;
       uint32_t bf[NT][G][2];
       if (have && pos + kStep <= limit_lo) {
-        weigh<D, NT, false>(x, ls, p, m, l, M, o, on);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int gr = 0; gr < G; ++gr)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              bf[nt][gr][h] = half2_bits(p[nt][2 * h] * ratio_v[h][gr],
-                                         p[nt][2 * h + 1] * ratio_v[h][gr]);
+        weigh<D, G, NT, false>(x, row_scale, ls, share, bf, ref, l, o, on, special, look);
       } else {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -751,16 +875,7 @@ cache_attend_kernel(const Level a) {
           for (int e = 0; e < 4; ++e)
             on[nt][e] = have && pos + k_tok + 8 * (e >> 1) <
                                     limit_of(row_first + nt * 8 + 2 * t + (e & 1));
-        weigh<D, NT, true>(x, ls, p, m, l, M, o, on);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int gr = 0; gr < G; ++gr)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              bf[nt][gr][h] =
-                  half2_bits(on[nt][2 * h] ? p[nt][2 * h] * ratio_v[h][gr] : 0.f,
-                             on[nt][2 * h + 1] ? p[nt][2 * h + 1] * ratio_v[h][gr] : 0.f);
+        weigh<D, G, NT, true>(x, row_scale, ls, share, bf, ref, l, o, on, special, look);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -851,14 +966,15 @@ cache_attend_kernel(const Level a) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int r = nt * 8 + 2 * t + k;
-        if (g == 0) row_lse[warp][r] = l[nt][k] == 0.f ? kNegInf : m[nt][k] + log2f(l[nt][k]);
+        const float m = k ? ref.m[nt].y : ref.m[nt].x, M = k ? ref.M[nt].y : ref.M[nt].x;
+        if (g == 0) row_lse[warp][r] = l[nt][k] == 0.f ? kNegInf : log2f(l[nt][k]) - m;
         const float inv = l[nt][k] == 0.f ? 0.f : 16777216.f / l[nt][k];
-        // 2^(M - m) as a square: M and m may lie further apart than one factor reaches
-        const float f = ex2(0.5f * (M[nt][k] - m[nt][k]));
 #pragma unroll
         for (int tile = 0; tile < D / 16; ++tile) {
           const int gr = tile / (GROUP / 16), i = tile % (GROUP / 16);
           const int d = gr * GROUP + g * (GROUP / 8) + 2 * i;
+          // 2^(M - m) / boost as a square: M and m may lie further apart than one factor reaches
+          const float f = ex2(0.5f * (m - M - (G == 1 ? 0.f : lg2(boost[gr]))));
           *reinterpret_cast<float2*>(res + r * C::kPad + d) =
               make_float2(o[nt][tile][k] * inv * f * f, o[nt][tile][2 + k] * inv * f * f);
         }

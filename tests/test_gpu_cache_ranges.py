@@ -79,6 +79,38 @@ def test_value_scales_far_apart_in_a_long_sequence(n):
     _attend(host, 9000, torch.zeros(n, 1, 64, dtype=torch.bfloat16))
 
 
+@pytest.mark.parametrize("dim,bits,group", [(128, 4, 32), (128, 8, 32), (128, 4, 64), (64, 8, 32)])
+@pytest.mark.parametrize("n", [1, 12])
+@pytest.mark.parametrize("size,other", [(1e-4, 0.0), (1e-8, 0.0), (1e-8, 1.0), (1e-4, 1e4),
+                                        (2.0 ** -40, 2.0 ** 40)])
+def test_groups_of_different_size(dim, bits, group, n, size, other):
+    """The first group's values are of size `other` (0: a head dimension padded up), the others'
+    of `size`; with even weights and with one token far above the rest."""
+    rng = np.random.default_rng(3)
+    k, v = (rng.standard_normal((700, dim)).astype(np.float32) for _ in range(2))
+    v *= np.where(np.arange(dim) < group, other, size).astype(np.float32)
+    host = _host(k, v, bits, group)
+    _attend(host, 700, torch.zeros(n, 1, dim, dtype=torch.bfloat16))
+    q = np.repeat(k[None, 400:401], n, 0) * np.float32(14 * dim ** 0.5 / (k[400] @ k[400]))
+    _attend(host, 700, torch.from_numpy(q).to(torch.bfloat16))      # a score of 14
+
+
+@pytest.mark.parametrize("dim,bits,group", FORMATS)
+@pytest.mark.parametrize("n", [1, 12])
+@pytest.mark.parametrize("size", [1e-4, 1e-8])
+def test_tokens_whose_values_are_zero(dim, bits, group, n, size):
+    """A third of the tokens has no values at all (their grid is [-1, 1] all the same)."""
+    rng = np.random.default_rng(4)
+    k, v = (rng.standard_normal((500, dim)).astype(np.float32) for _ in range(2))
+    v *= np.float32(size)
+    v[rng.random(500) < 0.33] = 0
+    v[37, group // 2:] = 0                # and one has some of them only
+    host = _host(k, v, bits, group)
+    _attend(host, 500, _queries(n, dim, 2))
+    v[:] = 0                              # and a sequence without any
+    _attend(_host(k, v, bits, group), 500, _queries(n, dim, 2))
+
+
 # ------------------------------------------------------------------------------------------------
 # lengths
 # ------------------------------------------------------------------------------------------------
