@@ -666,7 +666,7 @@ cache_attend_kernel(const Level a) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         row_scale[nt][k] =
-            __shfl_sync(0xffffffffu, down, (2 * t + k) * 4) * 16777216.f * a.scale_log2;
+            __shfl_sync(0xffffffffu, down, (2 * t + k) * 4) * 4096.f * a.scale_log2;
     }
 
     float o[NT][D / 16][4], l[NT][2];
@@ -713,7 +713,8 @@ cache_attend_kernel(const Level a) {
         else z4 = *reinterpret_cast<const uint32_t*>(grids + 128 + 4 * r);
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
-          sk[h][gr] = __uint_as_float(gr & 1 ? k2[gr / 2] & 0xFFFF0000u : k2[gr / 2] << 16);
+          // (2^12 of the codes' 2^24 here and 2^12 with the queries' scale: neither leaves fp32)
+          sk[h][gr] = 4096.f * __uint_as_float(gr & 1 ? k2[gr / 2] & 0xFFFF0000u : k2[gr / 2] << 16);
           nz[h][gr] = 8388608.f - __uint_as_float(prmt(z4, 0x4B000000u, 0x7540u | gr));
         }
       }

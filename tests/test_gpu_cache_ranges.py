@@ -111,6 +111,19 @@ def test_tokens_whose_values_are_zero(dim, bits, group, n, size):
     _attend(_host(k, v, bits, group), 500, _queries(n, dim, 2))
 
 
+@pytest.mark.parametrize("dim,bits,group", FORMATS)
+@pytest.mark.parametrize("n", [1, 12])
+@pytest.mark.parametrize("up", [124, 118, 100, -110])
+def test_queries_and_keys_of_opposite_size(dim, bits, group, n, up):
+    """Products of the usual size from queries of 2^up and keys of 2^-up."""
+    rng = np.random.default_rng(5)
+    k, v = (rng.standard_normal((90, dim)).astype(np.float32) for _ in range(2))
+    host = _host(k * np.float32(2.0 ** (2 - up)), v, bits, group)
+    q = (_queries(n, dim, 3).float() * 2.0 ** (up - 2)).to(torch.bfloat16)
+    assert torch.isfinite(q).all()
+    _attend(host, 90, q)
+
+
 # ------------------------------------------------------------------------------------------------
 # lengths
 # ------------------------------------------------------------------------------------------------
