@@ -495,7 +495,7 @@ gptq_status gptq_cache_attend_shared(const gptq_cache* cache, const gptq_cache_r
                                      int32_t* info_dev, void* stream);
 
 /* Workspace bytes of gptq_cache_attend (shared = 0) or gptq_cache_attend_shared (1) for n rows on
- * the current device; 0 for bad input. */
+ * the current device; 0 for bad input and for shapes that these calls refuse. */
 size_t gptq_cache_workspace_size(const gptq_cache* cache, int64_t n, int ratio, int shared);
 
 /* Workspace bytes needed by one call (GPTQ_WS_PREPARE or GPTQ_WS_QUANTIZE); 0 for bad input. */

@@ -417,6 +417,8 @@ gptq_status gptq_cache_attend_shared(const gptq_cache* cache, const gptq_cache_r
 size_t gptq_cache_workspace_size(const gptq_cache* cache, int64_t n, int ratio, int shared) {
   if (check_cache(cache, nullptr) != GPTQ_OK || n < 0 || n > INT32_MAX || ratio < 1 || ratio > 1024)
     return 0;
+  // what the calls refuse; below it no size leaves 64 bits
+  if (cache->heads * static_cast<int64_t>(ratio) > (1 << 18) || n * ratio > INT32_MAX) return 0;
   return cache_workspace_bytes(cache->heads, cache->dim, n, ratio, shared != 0);
 }
 

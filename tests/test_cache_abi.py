@@ -199,3 +199,16 @@ def test_one_row_has_the_stride_of_its_width():
         x = base.as_strided((1, 2, 128), (stride, 128, 1))
         assert _lib._heads_ld(x, "x", 2, 128) == 256
     assert _lib._heads_ld(base.as_strided((3, 2, 128), (264, 128, 1)), "x", 2, 128) == 264
+
+
+def test_no_workspace_size_for_refused_calls(built_lib):
+    """Shapes that the attention calls refuse have no size; the largest that they take have one that
+    fits in 64 bits."""
+    size = _lib.cache_workspace_size
+    for shared in (0, 1):
+        assert size(cache(heads=1 << 16), (1 << 31) - 1, 1024, shared) == 0
+        assert size(cache(heads=1024), 5, 512, shared) == 0
+        assert size(cache(), 1 << 22, 1000, shared) == 0
+        assert size(cache(), 1 << 30, 1, shared) > 0
+    n, ratio, heads = (1 << 31) // 1024 - 1, 1024, 256
+    assert size(cache(heads=heads), n, ratio, 1) > n * ratio * heads * 128 * 4
