@@ -83,14 +83,14 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float) -> np.ndar
 
 
 def attend_bound(q, kc, ks, kz, vc, vs, vz, scale: float, image16: bool = False,
-                 values16: bool = False, differences: bool = False):
+                 many_rows: bool = False):
     """One query [dim] over cached tokens: (the result, a bound on the error of a bf16 result of it),
     per dimension, for a kernel with fp32 sums and fp16 operands. The arithmetic written out, nothing
     measured. kc, vc: codes [tokens, dim]; ks, kz, vs, vz: their grids [tokens, groups].
 
     * The sums q . code take dim / 16 + 8 steps, each off by 2^-22 of the magnitudes it adds: x_t
       moves by (dim / 16 + 8) 2^-22 A_t, A_t = scale sum_groups s (sum |q| code + z sum |q|), or
-      with `differences`, where the sums are those of q (code - z), A_t = scale sum |q k|. The score,
+      with `many_rows`, where the sums are those of q (code - z), A_t = scale sum |q k|. The score,
       the largest one, the logarithm of a scale and their differences are fp32 numbers: 2^-22 of
       their magnitudes. The exponential and the products around it add 2^-20. With `image16` the
       keys are fp16 images of s (code - z), off by 2^-12 each: x_t moves by 2^-12 scale sum |q k|
@@ -101,13 +101,15 @@ def attend_bound(q, kc, ks, kz, vc, vs, vz, scale: float, image16: bool = False,
       being a token's largest scale. A group of a token's values that are all zero does not count.
       With `image16` each value is an image too, off
       by 2^-12 of itself or 2^-32 of the largest (key images likewise), and one unit holds for all
-      groups of a token. With `values16` only the values are images, off by 2^-12 of themselves or
-      2^-32 of their token's largest.
+      groups of a token. With `many_rows` (a shared prefix's own kernel) the values are images, off
+      by 2^-12 of themselves or 2^-32 of the largest of their 32 tokens (their own where that one is
+      2^13 and more above them), which the unit goes by, too; and where a row has several grids the
+      keys are images likewise.
     * The sum over tokens runs in steps of 16 and is joined from parts: (tokens / 16 + 64) 2^-22 of
       sum p |v|. Each step adds codes and takes zero points out: 2^-22 of sum p s (code + z) more.
       A code enters as an fp16 subnormal, which the tensor core aligns as if it were 2^-14, that is
       2^10 codes: each of a step's 16 products is cut at 2^-24 of that and the step's largest
-      weight, 16 * 2^-14 sum over steps of max p s. With `differences` the operands are normal.
+      weight, 16 * 2^-14 sum over steps of max p s. With `many_rows` the operands are normal.
     * The result is rounded to bf16: half a step, 2^-8 of the value that is rounded.
     """
     T, dim = kc.shape
@@ -122,7 +124,7 @@ def attend_bound(q, kc, ks, kz, vc, vs, vz, scale: float, image16: bool = False,
     out, mass = p @ v, p @ np.abs(v)
     aq = np.abs(q).reshape(G, -1)
     kq = scale * (np.abs(k) @ np.abs(q))
-    if differences:
+    if many_rows:
         A = kq
     else:
         A = scale * (ks.astype(np.float64) *
@@ -146,18 +148,24 @@ def attend_bound(q, kc, ks, kz, vc, vs, vz, scale: float, image16: bool = False,
         share = (live_s[some] / top_s[some, None]).max(0) if some.any() else np.zeros(G)
         unit = (p * top_s).max() * share                              # per group
         sums = np.einsum("tg,tgd->gd", ps, (vc + z).reshape(T, G, -1)).reshape(-1)
-        if differences:
+        def blocks(top):      # the largest of each token's 32, at most 2^13 times its own
+            most = np.pad(top, (0, -T % 32)).reshape(-1, 32).max(1).repeat(32)[:T]
+            return np.minimum(most, 2.0 ** 13 * top)
+        if many_rows:
+            if G > 1:
+                tops = np.pad(np.abs(k).max(1), (0, -T % 32)).reshape(-1, 32).max(1).repeat(32)[:T]
+                e += 2.0 ** -12 * kq + 2.0 ** -32 * scale * tops * np.abs(q).sum()
             bound = (p * e) @ np.abs(v - out) * (1 + 2 * (p * e).sum() + e[p > 2.0 ** -20].max())
         else:
             bound = 2 * e.max() * mass
         bound += mass * (2.0 ** -12 + steps) + 2.0 ** -22 * sums
-        if not differences:
+        if not many_rows:
             step = np.pad(ps, ((0, -T % 16), (0, 0))).reshape(-1, 16, G).max(1)
             bound += 2.0 ** -10 * np.repeat(step.sum(0), dim // G)
-        if values16:
-            top = np.abs(v).max(1)                                    # of a token
+        if many_rows:
+            top = blocks(np.abs(v).max(1))
             live = top > 0
-            bound += 2.0 ** -12 * mass + 2.0 ** -32 * (p @ top) + 2.0 ** -31 * (p * top).max() * \
+            bound += 2.0 ** -12 * mass + 2.0 ** -32 * (p @ top) + 2.0 ** -30 * (p * top).max() * \
                 (np.abs(v)[live] / top[live, None]).sum(0)
         else:
             bound += 2.0 ** -31 * np.repeat(unit, dim // G) * d.sum(0)

@@ -39,6 +39,16 @@ struct CacheRows {
 
 __device__ __forceinline__ float bf16_bits_to_float(uint32_t b) { return __uint_as_float(b << 16); }
 
+// Scale (bf16 bits) of a group whose values are all zero: 2 / (2^bits - 1), rounded up.
+template <int BITS>
+constexpr uint32_t kEmptyScale = BITS == 4 ? 0x3E09u : 0x3C01u;
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;

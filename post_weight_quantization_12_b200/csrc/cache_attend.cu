@@ -55,9 +55,6 @@ constexpr int kStep = 16;                   // tokens of one warp step
 constexpr int kStages = 3;                  // ring depth of a warp, in steps
 constexpr int kMaxResident = 4;             // CTAs per SM
 constexpr float kNegInf = -INFINITY;
-// Scale (bf16 bits) of a group whose values are all zero: 2 / (2^bits - 1), rounded up.
-template <int BITS>
-constexpr uint32_t kEmptyScale = BITS == 4 ? 0x3E09u : 0x3C01u;
 
 // A stage of the ring holds the codes of 16 tokens as they lie in the cache (K, then V, row after
 // row) and their grids. In shared memory the 16-byte chunks of a row are permuted: chunk c of row r
@@ -265,11 +262,6 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 // The G scales (bf16, 2 G bytes aligned) of a token, in pairs.
@@ -724,9 +716,9 @@ cache_attend_kernel(const Level a) {
       // scale that would push the others' operands out of fp16's range, and zero points times it
       // leave the rounding of their sum. Their share is 0.
       float ls[2], share[2][G];
-      bool special = false;
+      bool empty = false, over = false;
       auto v_grids = [&](auto careful) {
-        float over = 0.f;
+        float most = 0.f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int r = k_tok + 8 * h;
@@ -737,7 +729,7 @@ cache_attend_kernel(const Level a) {
             const uint32_t sv = gr & 1 ? v2[gr / 2] & 0xFFFF0000u : v2[gr / 2] << 16;
             share[h][gr] = __uint_as_float(sv);
             if constexpr (!careful.value) {
-              special |= sv == kEmptyScale<BITS> << 16;
+              empty |= sv == kEmptyScale<BITS> << 16;
             } else {
               constexpr int GB = GROUP * BITS / 8;
               const uint32_t z = zvp[r * G + gr] * (BITS == 4 ? 0x11111111u : 0x01010101u);
@@ -765,16 +757,16 @@ cache_attend_kernel(const Level a) {
 #pragma unroll
             for (int gr = 0; gr < G; ++gr) {
               share[h][gr] = share[h][gr] * inv * boost[gr];
-              over = fmaxf(over, share[h][gr]);
+              most = fmaxf(most, share[h][gr]);
             }
           }
         }
-        special |= over > 1.f;
+        over = most > 1.f;
       };
       v_grids(std::false_type{});
       auto look = [&]() {
-        v_grids(std::true_type{});
-        if constexpr (G > 1) {
+        if (__any_sync(0xffffffffu, empty)) v_grids(std::true_type{});
+        if (G > 1 && __any_sync(0xffffffffu, over)) {
           // only tokens that some row meets: what lies behind them must not matter
           const bool met0 = have && pos + k_tok < limit_hi, met1 = have && pos + k_tok + 8 < limit_hi;
 #pragma unroll
@@ -868,7 +860,7 @@ cache_attend_kernel(const Level a) {
         for (int e = 0; e < 4; ++e) on[nt][e] = true;
       uint32_t bf[NT][G][2];
       if (have && pos + kStep <= limit_lo) {
-        weigh<D, G, NT, false>(x, row_scale, ls, share, bf, ref, l, o, on, special, look);
+        weigh<D, G, NT, false>(x, row_scale, ls, share, bf, ref, l, o, on, empty || over, look);
       } else {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -876,7 +868,7 @@ cache_attend_kernel(const Level a) {
           for (int e = 0; e < 4; ++e)
             on[nt][e] = have && pos + k_tok + 8 * (e >> 1) <
                                     limit_of(row_first + nt * 8 + 2 * t + (e & 1));
-        weigh<D, G, NT, true>(x, row_scale, ls, share, bf, ref, l, o, on, special, look);
+        weigh<D, G, NT, true>(x, row_scale, ls, share, bf, ref, l, o, on, empty || over, look);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -969,15 +961,17 @@ cache_attend_kernel(const Level a) {
         const int r = nt * 8 + 2 * t + k;
         const float m = k ? ref.m[nt].y : ref.m[nt].x, M = k ? ref.M[nt].y : ref.M[nt].x;
         if (g == 0) row_lse[warp][r] = l[nt][k] == 0.f ? kNegInf : log2f(l[nt][k]) - m;
-        const float inv = l[nt][k] == 0.f ? 0.f : 16777216.f / l[nt][k];
+        const float inv = l[nt][k] == 0.f ? 0.f : 16777216.f * rcp(l[nt][k]);
 #pragma unroll
-        for (int tile = 0; tile < D / 16; ++tile) {
-          const int gr = tile / (GROUP / 16), i = tile % (GROUP / 16);
-          const int d = gr * GROUP + g * (GROUP / 8) + 2 * i;
+        for (int gr = 0; gr < G; ++gr) {
           // 2^(M - m) / boost as a square: M and m may lie further apart than one factor reaches
-          const float f = ex2(0.5f * (m - M - (G == 1 ? 0.f : lg2(boost[gr]))));
-          *reinterpret_cast<float2*>(res + r * C::kPad + d) =
-              make_float2(o[nt][tile][k] * inv * f * f, o[nt][tile][2 + k] * inv * f * f);
+          const float f = ex2(0.5f * (m - M - (G == 1 ? 0.f : lg2(boost[gr])))), f1 = inv * f;
+#pragma unroll
+          for (int i = 0; i < GROUP / 16; ++i) {
+            const int tile = gr * (GROUP / 16) + i;
+            *reinterpret_cast<float2*>(res + r * C::kPad + gr * GROUP + g * (GROUP / 8) + 2 * i) =
+                make_float2(o[nt][tile][k] * f1 * f, o[nt][tile][2 + k] * f1 * f);
+          }
         }
       }
     worker_sync();

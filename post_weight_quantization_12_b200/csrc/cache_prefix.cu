@@ -4,14 +4,22 @@
 // All query rows of a cache head (tokens x query heads of it) meet the same keys, so the codes are
 // unpacked once per 256 rows, into fp16 images that stay in shared memory:
 //   S = Q K^T     128 rows x 128 tokens, Q and the image of K both K-major
-//   P = 2^(S - m) fp16, written over S in tensor memory, where the second product reads it
+//   P = 2^(x + e - M) fp16, written over S in tensor memory, where the second product reads it
 //   O += P V      128 rows x D, the image of V with the dimensions contiguous (MN-major)
-// The image of a value is s' (q - z), q - z exact and one rounding to fp16 (2^-12), s' = s 2^(T - E)
-// with E the largest exponent among the tile's scales, so that the largest image stays below 65504:
-// values 2^-36 of the tile's largest are lost, whatever the scales are. The power of two goes back
-// in fp32: into the factor of S (K), into O's reference exponent (V, a running maximum).
-// m follows the running maximum of a row lazily: while S stays below m + 8 it is kept (weights up
-// to 2^8 fit in fp16), so O is rescaled in tensor memory only a few times.
+// K: where a row has one grid, its image is q - z, exact, and the score is x = S times the token's
+// scale, which the softmax groups read from shared memory: a rounding of the keys' images would move
+// a score by 2^-12 of sum |q k|, which is more than the output's own rounding where a few channels of
+// the keys stand out. Where a row has several grids no factor can be taken out: the image is
+// s' (q - z), one rounding (2^-12), s' = s 2^(T - E) with E the largest exponent among the scales of
+// 32 tokens, so that the largest image stays below 65504.
+// V: an image of that kind throughout, whose error stays 2^-12 of the value. Its power of two e goes
+// into the exponent of P, per 32 tokens, and per token where scales lie further apart, so a value far
+// above the others takes no bits of theirs unless the row gives it weight. Groups whose values are
+// all zero, whose grid is [-1, 1], do not count for E.
+// M, and m for the sum of 2^(x - m), are kept from tile to tile; the operands are made with the M at
+// hand and taken if the sum of 32 stays below 65000 (fp16 ends at 65504). Otherwise, and where m has
+// lost touch, the rows find their largest, M is set 2^7 below it, and O is rescaled in tensor memory:
+// a few times in all.
 //
 // A CTA (one per SM) holds two row tiles of 128 and goes over a run of 128-token tiles:
 //   warp 0           issues the products: PV(0), QK(0) of the next tile, PV(1), QK(1), so one
@@ -50,6 +58,11 @@ static_assert(kDqRows == 32, "a lane a row");
 constexpr int kMmaWarp = 0;
 constexpr int kThreads = 32 * (kDq0 + 2 * kDqWarps);
 constexpr float kNegInf = -INFINITY;
+// Registers a thread: what the block is launched with (65,536 over its threads), and what the four
+// warps in front give to the softmax groups' sixteen, whose 64 products a row and thread do not fit
+// otherwise (first case below: 153 us without, 148 with; 88 registers with less for unpacking 151).
+constexpr int kLaunchRegs = 72, kMmaRegs = 40, kSoftmaxRegs = 80;
+static_assert(kMmaRegs + 4 * kSoftmaxRegs + 2 * kLaunchRegs <= 7 * kLaunchRegs);
 
 struct Prefix {
   CacheView cache;
@@ -67,13 +80,34 @@ struct Prefix {
   int32_t* info;
 };
 
+// What the warps share beside the tiles.
+struct Side {
+  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], g_full[2];
+  uint64_t s_full[2], p_full[2], pv_done[2], mma_done;
+  // Of step s in slot s % 2. What the images of its tokens lack: K's factor, a token's (with 2^-14 in
+  // it), or where a row has several grids 32 tokens'; V's power of two, 32 tokens' (as a number; -inf
+  // where they have none in common) and a token's (bf16 bits).
+  alignas(16) uint32_t valid[2][4];        // tokens that count
+  alignas(16) float k_scale[2][kTok];
+  alignas(16) float v_exp[2][4];
+  uint16_t v_scale[2][kTok];
+  float row_x[2][128];                     // of (row tile, row): what its halves exchange
+  uint32_t tmem_base;
+  volatile int abort;
+};
+constexpr float kFirst = -3e38f;           // a reference before the first score
+constexpr float kMostSum = 65000.f;        // of 32 operands, each below 65504
+constexpr float kMostLog = 15.9882f;       // its logarithm
+
 template <int D, int BITS>
 struct Smem {
   static constexpr int kTileBytes = kTok * D * 2;         // an operand tile: D / 64 halves of 16 KB
   static constexpr int kCodeBytes = kTok * D * BITS / 8;  // a tile's codes of K or V
   static constexpr int kAhead = BITS == 4 ? 2 : 1;        // steps whose codes are on the way
-  // Q 0, Q 1, K 0, K 1, V 0, V 1, codes
-  static constexpr int kBytes = 6 * kTileBytes + kAhead * 2 * kCodeBytes + 1024;
+  // Q 0, Q 1, K 0, K 1, V 0, V 1, codes, then Side
+  static constexpr int kSide = 6 * kTileBytes + kAhead * 2 * kCodeBytes;
+  static constexpr int kBytes = kSide + static_cast<int>(sizeof(Side));
+  static_assert(kBytes <= 227 * 1024);
 };
 
 __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
@@ -95,6 +129,15 @@ __device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
                  "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
+}
+// All four warps of a group, at the same place.
+template <int N>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 // One lane of a converged warp, the same at every call.
 __device__ __forceinline__ bool elect_one() {
@@ -151,7 +194,7 @@ __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
@@ -192,22 +235,18 @@ cache_prefix_kernel(const Prefix a) {
   constexpr int G = D / GROUP, RB = D * BITS / 8;
   using SM = Smem<D, BITS>;
   constexpr int kTile = SM::kTileBytes;
-  constexpr int kTop = BITS == 4 ? 11 : 7;       // images below 2^(kTop + 1) (2^BITS - 1) < 65504
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_align<1024>(smem_raw);
+  // exponent of the largest scale in a token's images: below 2^(kTop + 1) (2^BITS - 1) < 65504
+  constexpr int kTop = BITS == 4 ? 11 : 7;
+  extern __shared__ __align__(1024) uint8_t smem[];    // (operand tiles: multiples of 1024 bytes)
   auto q_tile = [&](int i) { return smem + i * kTile; };
   auto k_tile = [&](int b) { return smem + (2 + b) * kTile; };
   auto v_tile = [&](int b) { return smem + (4 + b) * kTile; };
   auto code_slot = [&](int b, int h) { return smem + 6 * kTile + (2 * b + h) * SM::kCodeBytes; };
-  __shared__ __align__(8) uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2], mma_done;
-  __shared__ __align__(16) uint32_t valid[4][4];   // of step s in slot s % 4: tokens that count
-  __shared__ int k_exp[4], v_exp[4];               // ... and the exponents of its images
-  __shared__ uint32_t warp_top[2][2][kDqWarps][2];   // of the unpackers of K and V
-  __shared__ float row_x[2][128];                  // of (row tile, row): what its halves exchange
-  __shared__ uint32_t tmem_base_sh;
-  __shared__ volatile int abort_flag;
-
+  Side& sh = *reinterpret_cast<Side*>(smem + SM::kSide);
+  uint64_t *q_full = sh.q_full, *k_full = sh.k_full, *k_empty = sh.k_empty, *v_full = sh.v_full;
+  uint64_t *v_empty = sh.v_empty, *g_full = sh.g_full, *s_full = sh.s_full, *p_full = sh.p_full;
+  uint64_t* pv_done = sh.pv_done;
+  volatile int* abort_flag = &sh.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
@@ -216,22 +255,23 @@ cache_prefix_kernel(const Prefix a) {
       mbar_init(&k_empty[b], 1);
       mbar_init(&v_full[b], 32 * kDqWarps);
       mbar_init(&v_empty[b], 1);
+      mbar_init(&g_full[b], 32 * kDqWarps);
       mbar_init(&s_full[b], 1);
       mbar_init(&p_full[b], 256);
       mbar_init(&pv_done[b], 1);
     }
-    mbar_init(&mma_done, 1);
-    abort_flag = 0;
+    mbar_init(&sh.mma_done, 1);
+    sh.abort = 0;
     fence_mbarrier_init();
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(&tmem_base_sh, 512);
+    tmem_alloc(&sh.tmem_base, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_base_sh;
+  const uint32_t tmem = sh.tmem_base;
   auto tm_s = [&](int i) { return tmem + 128 * i; };   // S; P over the first half of each half
   auto tm_o = [&](int i) { return tmem + 256 + D * i; };
   // What this kernel reads (queries, cache) was complete before the kernel in front of it, which
@@ -241,6 +281,7 @@ cache_prefix_kernel(const Prefix a) {
   int32_t* info = a.info;
 
   if (warp >= kSm0 && warp < kDq0) {
+    registers_up<kSoftmaxRegs>();
     // ---- softmax group i: threads r and r + 128 of it share row r, tokens 64 hf .. of each tile ----
     const int i = (warp - kSm0) >> 3, hf = ((warp - kSm0) >> 2) & 1;
     const int r = (warp & 3) * 32 + lane;
@@ -249,13 +290,13 @@ cache_prefix_kernel(const Prefix a) {
     auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory"); };
     // the other half's value: one place for both, first for the one, then for the other
     auto exchange = [&](float x) -> float {
-      if (hf == 0) row_x[i][r] = x;
+      if (hf == 0) sh.row_x[i][r] = x;
       pair_sync();
-      const float y = row_x[i][r];
+      const float y = sh.row_x[i][r];
       pair_sync();
-      if (hf == 1) row_x[i][r] = x;
+      if (hf == 1) sh.row_x[i][r] = x;
       pair_sync();
-      const float z = row_x[i][r];
+      const float z = sh.row_x[i][r];
       pair_sync();
       return hf == 0 ? z : y;
     };
@@ -296,7 +337,9 @@ cache_prefix_kernel(const Prefix a) {
         const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
         // a negative scale goes into Q, so the largest score is the largest product
         const float up = (e > 127 ? 1.f : pow2(14 - e)) * (a.scale_log2 < 0.f ? -1.f : 1.f);
-        row_c = (e > 127 ? 1.f : pow2(e - 14)) * fabsf(a.scale_log2);
+        // (2^14 makes up for the 2^-14 of the keys' factors; never 0: a token that does not count
+        // has a product of -inf)
+        row_c = fmaxf((e > 127 ? 16384.f : pow2(e)) * fabsf(a.scale_log2), 1.17549435e-38f);
         if (w.two || i == 0) {
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
@@ -307,7 +350,14 @@ cache_prefix_kernel(const Prefix a) {
               f[2 * k] = __uint_as_float(x[k] << 16) * up;
               f[2 * k + 1] = __uint_as_float(x[k] & 0xFFFF0000u) * up;
             }
-            // in the order that 4-bit codes come out of their word
+            // in the order that 4-bit codes come out of their word; every other one 16 times too
+            // large, if its image has no scale
+            if (BITS == 4 && G == 1) {
+              f[1] *= 0.0625f;
+              f[3] *= 0.0625f;
+              f[5] *= 0.0625f;
+              f[7] *= 0.0625f;
+            }
             const uint4 h = BITS == 4 ? make_uint4(half2_bits(f[0], f[4]), half2_bits(f[1], f[5]),
                                                    half2_bits(f[2], f[6]), half2_bits(f[3], f[7]))
                                       : make_uint4(half2_bits(f[0], f[1]), half2_bits(f[2], f[3]),
@@ -320,18 +370,19 @@ cache_prefix_kernel(const Prefix a) {
           mbar_arrive(&q_full[i]);
         }
       }
-      float m = kNegInf, l = 0.f;       // of the row; l: this half's share
-      int e_ref = -1000;
+      // references of the row, and this half's share of the sum of 2^(x - m)
+      float m = kFirst, M = kFirst, l = 0.f;
       for (int k = 0; k < my_steps; ++k, ++c_step) {
-        const int slot = (g_base + step_of(w, i, k)) & 3;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&s_full[i], c_step & 1, &abort_flag, info));
+        const uint32_t gs = g_base + step_of(w, i, k);
+        const int slot = gs & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&g_full[slot], (gs >> 1) & 1u, abort_flag,
+                                                       info) &&
+                                     mbar_wait_bounded(&s_full[i], c_step & 1, abort_flag, info));
         tc_fence_after();
-        const int e_new = v_exp[slot];
-        // (never 0: a token that does not count has a product of -inf)
-        const float xs = fmaxf(row_c * pow2(k_exp[slot]), 1.17549435e-38f);
         const uint32_t ts = tm_s(i) + lane_base + 64 * hf;
-        uint32_t v[32];
-        const uint2 vm = *reinterpret_cast<const uint2*>(&valid[slot][2 * hf]);
+        const float* k_scale = sh.k_scale[slot] + (G == 1 ? 64 : 2) * hf;
+        const float2 e_v = *reinterpret_cast<const float2*>(&sh.v_exp[slot][2 * hf]);
+        const uint2 vm = *reinterpret_cast<const uint2*>(&sh.valid[slot][2 * hf]);
         if ((vm.x & vm.y) != 0xFFFFFFFFu) {
           // tokens that do not count: their products become -inf
 #pragma unroll 1
@@ -347,37 +398,94 @@ cache_prefix_kernel(const Prefix a) {
           }
           tmem_wait_st();
         }
-        // largest product of the row's half: tokens 32 .., then 0 .., which stay in registers
-        float top = kNegInf, top_b = kNegInf;
-        auto max32 = [&]() {
+        // operands 2^(x + e - M) of 32 tokens at a time (e: V's power of two) and their sum
+        uint32_t p[2][16];
+        float sum[2];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const float c = G == 1 ? row_c : fmaxf(row_c * k_scale[hh], 1.17549435e-38f);
+          const float ref = (hh ? e_v.y : e_v.x) - M;
+          const float2 c2 = make_float2(c, c), ref2 = make_float2(ref, ref);
+          float2 sa = make_float2(0.f, 0.f), sb = sa;
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(ts + 32 * hh, v);
+          tmem_wait_ld(v);
 #pragma unroll
           for (int t = 0; t < 32; t += 4) {
-            top = fmaxf(fmaxf(top, __uint_as_float(v[t])), __uint_as_float(v[t + 1]));
-            top_b = fmaxf(fmaxf(top_b, __uint_as_float(v[t + 2])), __uint_as_float(v[t + 3]));
+            float2 xa = make_float2(__uint_as_float(v[t]), __uint_as_float(v[t + 1]));
+            float2 xb = make_float2(__uint_as_float(v[t + 2]), __uint_as_float(v[t + 3]));
+            if constexpr (G == 1) {
+              const float4 ks = *reinterpret_cast<const float4*>(k_scale + 32 * hh + t);
+              xa = mul2(xa, make_float2(ks.x, ks.y));
+              xb = mul2(xb, make_float2(ks.z, ks.w));
+            }
+            const float2 ya = fma2(xa, c2, ref2), yb = fma2(xb, c2, ref2);
+            const float2 pa = make_float2(ex2(ya.x), ex2(ya.y));
+            const float2 pb = make_float2(ex2(yb.x), ex2(yb.y));
+            sa = add2(sa, pa);
+            sb = add2(sb, pb);
+            p[hh][t / 2] = half2_bits(pa.x, pa.y);
+            p[hh][t / 2 + 1] = half2_bits(pb.x, pb.y);
           }
-        };
-        tmem_ld_32x32b_x32(ts + 32, v);
-        tmem_wait_ld(v);
-        max32();
-        tmem_ld_32x32b_x32(ts, v);
-        tmem_wait_ld(v);
-        max32();
-        top = fmaxf(top, top_b);
-        top = top == kNegInf ? kNegInf : top * xs;
-        // both warps of the rows go one way: on, or through a new reference (or out, after an error).
-        if (named_barrier_or(pair, 64, !ok || top > m + 8.f || e_new > e_ref)) {
+          sa = add2(sa, sb);
+          sum[hh] = sa.x + sa.y;
+        }
+        // Taken as they are if M allows them and the weights are theirs times 2^(M - e - m), a power
+        // that neither has lost them (a weight below 2^-62 of the row's unit may be 0) nor is beyond
+        // fp32. Both warps of the rows go one way (or out, after an error).
+        const bool over = sum[0] > kMostSum || sum[1] > kMostSum;
+        const float d0 = M - e_v.x - m, d1 = M - e_v.y - m;
+        if (!named_barrier_or(pair, 64, !ok || over || d0 > 64.f || d1 > 64.f)) {
+          l += fmaf(sum[0], ex2(d0), sum[1] * ex2(d1));
+          // written over the S that they come from: 64 tokens' over the first 32 columns of their
+          // half
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[8];
+#pragma unroll
+            for (int t = 0; t < 8; ++t) x[t] = p[c / 2][8 * (c & 1) + t];
+            tmem_st_32x32b_x8(ts + 8 * c, x);
+          }
+        } else {
           if (named_barrier_or(pair, 64, !ok)) {
             ok = false;
             break;
           }
-          const float m_new = fmaxf(m, fmaxf(top, exchange(top)));
-          const float f = m == kNegInf ? 0.f : ex2(m - m_new);
-          l *= f;
-          m = m_new;
+          const uint16_t* v_scale = sh.v_scale[slot] + 64 * hf;
+          // score and power of two of token t, whose product is v
+          auto score = [&](uint32_t v, int t) {
+            return G == 1 ? __uint_as_float(v) * k_scale[t] * row_c
+                          : __uint_as_float(v) * fmaxf(row_c * k_scale[t >> 5], 1.17549435e-38f);
+          };
+          auto power = [&](int t) { return static_cast<float>(v_scale[t] >> 7) - 127.f; };
+          float top = kNegInf, top_M = kNegInf;
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t x[8];
+            tmem_ld_32x32b_x8(ts + 8 * c, x);
+            tmem_wait_ld(x);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+              const float y = score(x[t], 8 * c + t);
+              top = fmaxf(top, y);
+              top_M = fmaxf(top_M, y + power(8 * c + t));
+            }
+          }
+          top = fmaxf(top, exchange(top));
+          top_M = fmaxf(top_M, exchange(top_M));
+          const float any_over = over ? 1.f : 0.f;
+          const bool raise = fmaxf(any_over, exchange(any_over)) > 0.f || top_M > M + kMostLog;
+          if (top > m + 64.f) {
+            l *= ex2(m - top);
+            m = top;
+          }
+          // a new reference lies 2^7 below the largest operand
+          const float M_new = raise ? fmaxf(M, top_M - 7.f) : M;
+          const float f = ex2(M - M_new);
+          M = M_new;
           if (k > 0) {
             // O of the steps so far: the products that made it are complete (they were issued
             // before this step's S)
-            const float fo = f * (e_ref < e_new - 120 ? 0.f : pow2(e_ref - e_new));
             const uint32_t to = tm_o(i) + lane_base + hf * (D / 2);
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
@@ -385,38 +493,29 @@ cache_prefix_kernel(const Prefix a) {
               tmem_ld_32x32b_x8(to + 8 * c, x);
               tmem_wait_ld(x);
 #pragma unroll
-              for (int t = 0; t < 8; ++t) x[t] = __float_as_uint(__uint_as_float(x[t]) * fo);
+              for (int t = 0; t < 8; ++t) x[t] = __float_as_uint(__uint_as_float(x[t]) * f);
               tmem_st_32x32b_x8(to + 8 * c, x);
             }
           }
-          e_ref = e_new;
-        }
-        // weights, written over the S that they come from: 64 tokens' over the first 32 columns of
-        // their half, of which what is still to be read lies behind
-        const float ref = m == kNegInf ? 0.f : m;
-        const float2 xs2 = make_float2(xs, xs), ref2 = make_float2(-ref, -ref);
-        float2 sum = make_float2(0.f, 0.f), sum_b = sum;
-        auto weigh = [&](int c) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t p[8];
+          // (16 tokens' operands go over the S of tokens already read)
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[8], y[8], z[8];
+            tmem_ld_32x32b_x8(ts + 16 * c, x);
+            tmem_ld_32x32b_x8(ts + 16 * c + 8, y);
+            tmem_wait_ld(x);
+            tmem_wait_ld(y);
 #pragma unroll
             for (int t = 0; t < 16; t += 2) {
-              const float2 y = fma2(make_float2(__uint_as_float(v[16 * x + t]),
-                                                __uint_as_float(v[16 * x + t + 1])), xs2, ref2);
-              const float2 e = make_float2(ex2(y.x), ex2(y.y));
-              if (t & 2) sum = add2(sum, e); else sum_b = add2(sum_b, e);
-              p[t / 2] = half2_bits(e.x, e.y);
+              const int at = 16 * c + t;
+              const float s0 = score(t < 8 ? x[t] : y[t - 8], at);
+              const float s1 = score(t < 8 ? x[t + 1] : y[t - 7], at + 1);
+              l += ex2(s0 - m) + ex2(s1 - m);
+              z[t / 2] = half2_bits(ex2(s0 + (power(at) - M)), ex2(s1 + (power(at + 1) - M)));
             }
-            tmem_st_32x32b_x8(ts + 16 * c + 8 * x, p);
+            tmem_st_32x32b_x8(ts + 8 * c, z);
           }
-        };
-        weigh(0);
-        tmem_ld_32x32b_x32(ts + 32, v);
-        tmem_wait_ld(v);
-        weigh(1);
-        sum = add2(sum, sum_b);
-        l += sum.x + sum.y;
+        }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&p_full[i]);
@@ -428,17 +527,17 @@ cache_prefix_kernel(const Prefix a) {
       float lse = kNegInf;
       if (my_steps > 0) {
         ok = __all_sync(0xffffffffu,
-                        mbar_wait_bounded(&pv_done[i], (c_step - 1) & 1, &abort_flag, info));
+                        mbar_wait_bounded(&pv_done[i], (c_step - 1) & 1, abort_flag, info));
         if (named_barrier_or(pair, 64, !ok)) {
           ok = false;
           break;
         }
         tc_fence_after();
         l += exchange(l);
-        lse = l == 0.f ? kNegInf : (m == kNegInf ? 0.f : m) + log2f(l);
+        lse = l == 0.f ? kNegInf : m + log2f(l);
         const float f = l == 0.f ? 0.f : 1.f / l;
-        // 2^e_ref in two factors: each within fp32's normal range
-        const float f0 = pow2(e_ref / 2), f1 = pow2(e_ref - e_ref / 2);
+        // 2^(M - m) as a square: M and m may lie further apart than one factor reaches
+        const float f2 = ex2(0.5f * (M - m));
         float* dst = a.part + (slot * 128 + r) * D + hf * (D / 2);
 #pragma unroll 1
         for (int c = 0; c < D / 16; ++c) {
@@ -446,7 +545,7 @@ cache_prefix_kernel(const Prefix a) {
           tmem_ld_32x32b_x8(tm_o(i) + lane_base + hf * (D / 2) + 8 * c, x);
           tmem_wait_ld(x);
 #pragma unroll
-          for (int t = 0; t < 8; ++t) x[t] = __float_as_uint(__uint_as_float(x[t]) * f * f0 * f1);
+          for (int t = 0; t < 8; ++t) x[t] = __float_as_uint(__uint_as_float(x[t]) * f * f2 * f2);
           if (live) {
             uint4 lo, hi;
             if constexpr (BITS == 4) {      // columns hold dims 0 4 1 5 2 6 3 7 of each eight
@@ -528,9 +627,9 @@ cache_prefix_kernel(const Prefix a) {
       }
       cp_commit();
     };
-    // scales (bf16 pairs) and zeros (bytes) of the warp's row `lane`; the unpackers of K take V's
-    // scales too: the softmax groups need both exponents with S
-    uint32_t sc[kS], sv[kS], zr;
+    // Of the warp's row `lane`: the zeros (bytes) of this half, its own scales (bf16 pairs) and, for
+    // the unpackers of V, K's: they tell the softmax groups what the token's images lack.
+    uint32_t sc[kS], sk[kS], zr;
     auto load_scales = [&](const uint16_t* s, uint32_t (&x)[kS]) {
       if constexpr (G == 1) {
         x[0] = __ldg(s);
@@ -544,21 +643,25 @@ cache_prefix_kernel(const Prefix a) {
     };
     auto load_grids = [&](int64_t row) {
       const int64_t from = max(row, static_cast<int64_t>(0)) * G;
-      load_scales(half.scales + from, sc);
-      if (h == 0) load_scales(a.cache.half[1].scales + from, sv);
+      if (G > 1 || h == 1) load_scales(half.scales + from, sc);
+      if (h == 1) load_scales(a.cache.half[0].scales + from, sk);
       const uint8_t* z = half.zeros + from;
       if constexpr (G == 1) zr = __ldg(z);
       else if constexpr (G == 2) zr = __ldg(reinterpret_cast<const uint16_t*>(z));
       else zr = __ldg(reinterpret_cast<const uint32_t*>(z));
     };
+    auto scale_of = [&](const uint32_t (&x)[kS], int gr) -> uint32_t {      // as fp32 bits
+      return gr & 1 ? x[gr / 2] & 0xFFFF0000u : x[gr / 2] << 16;
+    };
+    // a token's largest scale, as fp32 bits; not of the ones that are not finite
     auto top_of = [&](const uint32_t (&x)[kS]) -> uint32_t {
-      uint32_t top = 0;              // largest scale, as bits; not the ones that are not finite
+      uint32_t top = 0;
 #pragma unroll
-      for (int k = 0; k < G; ++k) {
-        const uint32_t y = k & 1 ? x[k / 2] >> 16 : x[k / 2] & 0xFFFFu;
-        top = max(top, y < 0x7F80u ? y : 0u);
+      for (int gr = 0; gr < G; ++gr) {
+        const uint32_t y = scale_of(x, gr);
+        top = max(top, y < 0x7F800000u ? y : 0u);
       }
-      return __reduce_max_sync(0xffffffffu, top);
+      return top;
     };
     bool ok = true;
     uint32_t gs = 0;
@@ -576,41 +679,20 @@ cache_prefix_kernel(const Prefix a) {
     look(ahead);
     next(ahead);
     load_grids(rows[0]);
-    int v_ref = -1000, v_unit = -1;
     for (; now.u < a.units; ++gs) {
-      const int b = gs & 1, slot = gs & 3;
+      const int b = gs & 1;
       const int cb = SM::kAhead == 1 ? 0 : b;
       const uint32_t ph = (gs >> 1) & 1u;
-      if (now.u != v_unit) v_ref = -1000;
-      v_unit = now.u;
       const bool counts = rows[0] >= 0;
-      // a token that does not count: zero scales, so its images are zeros
-      if (!counts) {
-#pragma unroll
-        for (int k = 0; k < kS; ++k) sc[k] = sv[k] = 0;
-      }
-      // the tile's largest scales
-      const uint32_t top_own = top_of(sc), top_v = h == 0 ? top_of(sv) : top_own;
-      if (lane == 0) {
-        warp_top[h][gs & 1][dw][0] = top_own;
-        warp_top[h][gs & 1][dw][1] = top_v;
-      }
-      // all the warps leave together if one of them gave up
-      if (named_barrier_or(h == 0 ? 1 : 10, 32 * kDqWarps, !ok)) break;
-      uint32_t top[2] = {0, 0};
-#pragma unroll
-      for (int x = 0; x < kDqWarps; ++x) {
-        top[0] = max(top[0], warp_top[h][gs & 1][x][0]);
-        top[1] = max(top[1], warp_top[h][gs & 1][x][1]);
-      }
-      v_ref = max(v_ref, max(static_cast<int>(top[1] >> 7) - 127, -107));
-      const int e = h == 0 ? max(static_cast<int>(top[0] >> 7) - 127, -107) : v_ref;
-      // this step's grids move on to make room for the next one's
-      uint32_t s_h[kS];
-#pragma unroll
-      for (int k = 0; k < kS; ++k) s_h[k] = sc[k];
-      const uint32_t z_h = zr;
       const uint32_t counting = __ballot_sync(0xffffffffu, counts);
+      // this step's grids move on to make room for the next one's
+      uint32_t s_h[kS], k_h[kS];
+#pragma unroll
+      for (int k = 0; k < kS; ++k) {
+        s_h[k] = sc[k];
+        k_h[k] = sk[k];
+      }
+      const uint32_t z_h = zr;
       next(now);
       rows[SM::kAhead] = resolve();
       look(ahead);
@@ -619,74 +701,145 @@ cache_prefix_kernel(const Prefix a) {
       {
         cp_wait<SM::kAhead - 1>();
         __syncwarp();
-        if (ok) ok = mbar_wait_bounded(h == 0 ? &k_empty[b] : &v_empty[b], ph ^ 1u, &abort_flag,
-                                       info);
-        if (h == 0) {
-          // slot s % 4 was last read by step s - 4's softmax; k_empty of step s - 2 is past it
-          if (lane == 0) valid[slot][dw] = counting;
-          if (dw == 0 && lane == 0) {
-            k_exp[slot] = e - kTop;
-            v_exp[slot] = v_ref - kTop;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(h == 0 ? &k_empty[b] : &v_empty[b], ph ^ 1u,
+                                                       abort_flag, info));
+        if (!ok) break;
+        const uint8_t* warp_codes = code_slot(cb, h) + dw * (SM::kCodeBytes / kDqWarps);
+        const uint8_t* src = warp_codes + lane * 16;
+        uint8_t* tile = h == 0 ? k_tile(b) : v_tile(b);
+        // A group of V without values has the grid [-1, 1], a scale that would push the others' out
+        // of fp16's range: it counts as 0.
+        if (h == 1) {
+          bool empty[G], any = false;
+#pragma unroll
+          for (int gr = 0; gr < G; ++gr) {
+            empty[gr] = counts && scale_of(s_h, gr) == kEmptyScale<BITS> << 16;
+            any |= empty[gr];
+          }
+          if (__any_sync(0xffffffffu, any)) {
+            // row `lane`: lane t of row g copied it in access g / RPI
+#pragma unroll
+            for (int v = 0; v < kVec; ++v)
+#pragma unroll
+              for (int x = 0; x < LPR; ++x) {
+                const int gr = (BITS == 4 ? 32 * x : 16 * x + v * (D / 2)) / GROUP;
+                const uint32_t z =
+                    (z_h >> (8 * gr) & 0xFFu) * (BITS == 4 ? 0x11111111u : 0x01010101u);
+                const uint4 c = *reinterpret_cast<const uint4*>(
+                    warp_codes + ((lane / RPI * kVec + v) * 32 + lane % RPI * LPR + x) * 16);
+                if ((c.x ^ z) | (c.y ^ z) | (c.z ^ z) | (c.w ^ z)) {
+#pragma unroll
+                  for (int y = 0; y < G; ++y)
+                    if (y == gr) empty[y] = false;
+                }
+              }
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+              if (empty[gr]) s_h[gr / 2] &= gr & 1 ? 0x0000FFFFu : 0xFFFF0000u;
           }
         }
-        const float unit = pow2(max(kTop - e, -126));
-        const uint8_t* src = code_slot(cb, h) + dw * (SM::kCodeBytes / kDqWarps) + lane * 16;
-        uint8_t* tile = h == 0 ? k_tile(b) : v_tile(b);
+        // a token that does not count has scales of 0
+        if (!counts) {
 #pragma unroll
-        for (int k = 0; k < KI; ++k) {
-          const int rl = k * RPI + g, row = dw * kDqRows + rl;
-          uint32_t sw[kS];
+          for (int k = 0; k < kS; ++k) s_h[k] = 0;
+        }
+        // The images carry scales relative to a power of two, the one above the largest scale of the
+        // warp's 32 tokens, so that the largest image stays below 65504; K's, where a row has one
+        // grid, none at all: codes less their zero points are exact. Where scales of V lie more than
+        // 2^12 apart, each token has a power of its own.
+        auto exponent = [&](uint32_t top, int least) {
+          return max(static_cast<int>(top >> 23) - 127, least);
+        };
+        const uint32_t top = top_of(s_h);
+        int e = 0;
+        if (G > 1 || h == 1) e = exponent(__reduce_max_sync(0xffffffffu, top), h == 0 ? -107 : -96);
+        if (h == 1) {
+          const bool wide = __any_sync(0xffffffffu, top != 0 && exponent(top, -126) < e - 12);
+          if (wide) e = exponent(top, -96);
+          if constexpr (G == 1) {
+            sh.k_scale[b][dw * kDqRows + lane] =
+                counts ? __uint_as_float(k_h[0] << 16) * 6.1035156e-5f : 1.f;
+          } else {
+            const uint32_t k_top = __reduce_max_sync(0xffffffffu, counts ? top_of(k_h) : 0u);
+            if (lane == 0) sh.k_scale[b][dw] = pow2(exponent(k_top, -107) - kTop) * 6.1035156e-5f;
+          }
+          sh.v_scale[b][dw * kDqRows + lane] = static_cast<uint16_t>((e - kTop + 127) << 7);
+          if (lane == 0) {
+            sh.v_exp[b][dw] = wide ? kNegInf : static_cast<float>(e - kTop);
+            sh.valid[b][dw] = counting;
+          }
+          mbar_arrive(&g_full[b]);
+        }
+        uint32_t r_h[kS] = {};
+        if (G > 1 || h == 1) {
+          const float unit = pow2(kTop - e);
 #pragma unroll
-          for (int x = 0; x < kS; ++x) sw[x] = __shfl_sync(0xffffffffu, s_h[x], rl);
-          const uint32_t zw = __shfl_sync(0xffffffffu, z_h, rl);
+          for (int k = 0; k < kS; ++k)
+            r_h[k] = half2_bits(__uint_as_float(s_h[k] << 16) * unit,
+                                __uint_as_float(s_h[k] & 0xFFFF0000u) * unit);
+        }
+        auto unpack = [&](auto plain) {            // plain: images without scales
 #pragma unroll
-          for (int v = 0; v < kVec; ++v) {
-            const int group = dim_of(v) / GROUP;
-            const uint32_t s_w = kS == 2 && (group & 2) ? sw[kS - 1] : sw[0];
-            const uint32_t z = zw >> (8 * group) & 0xFFu;
-            const float f = __uint_as_float(group & 1 ? s_w & 0xFFFF0000u : s_w << 16) * unit;
-            const uint32_t s2 = half2_bits(f, f);
-            const uint32_t z2 = (0x6400u + z) * 0x00010001u;            // 1024 + z, exact
-            const uint4 w4 = *reinterpret_cast<const uint4*>(src + (k * kVec + v) * 512);
-            uint32_t wd[4] = {w4.x, w4.y, w4.z, w4.w};
-            // this piece's image: chunks of eight dims from chunk c0 of its 64-dim half
-            uint8_t* dst = tile + (dim_of(v) >> 6) * (kTok * 128) + row * 128;
-            const uint32_t c0 = (dim_of(v) & 63) >> 3;
-            if constexpr (BITS == 4) {
-              // lanes t and t + 2 store to different halves, of the same banks: they take their
-              // four chunks in another order, so the eight lanes of a store meet all the banks
-              const uint32_t flip = D == 128 ? (t & 2) : 0;
-              if (D == 128 && flip) {
-                uint32_t x = wd[0]; wd[0] = wd[2]; wd[2] = x;
-                x = wd[1]; wd[1] = wd[3]; wd[3] = x;
-              }
-              const uint32_t s16 = mul2(s2, 0x2C002C00u);               // s / 16
-              const uint32_t z16 = (0x6400u + 16 * z) * 0x00010001u;    // 1024 + 16 z
+          for (int k = 0; k < KI; ++k) {
+            const int rl = k * RPI + g, row = dw * kDqRows + rl;
+            uint32_t sw[kS];
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const uint32_t x = wd[c], x8 = x >> 8;
-                const uint4 y = make_uint4(
-                    mul2(sub2((x & 0x000F000Fu) | 0x64006400u, z2), s2),       // codes 0, 4
-                    mul2(sub2((x & 0x00F000F0u) | 0x64006400u, z16), s16),     // 1, 5, times 16
-                    mul2(sub2((x8 & 0x000F000Fu) | 0x64006400u, z2), s2),      // 2, 6
-                    mul2(sub2((x8 & 0x00F000F0u) | 0x64006400u, z16), s16));   // 3, 7
-                *reinterpret_cast<uint4*>(dst + (((c0 + (c ^ flip)) ^ (row & 7)) << 4)) = y;
-              }
-            } else {
+            for (int x = 0; x < kS; ++x) sw[x] = __shfl_sync(0xffffffffu, r_h[x], rl);
+            const uint32_t zw = __shfl_sync(0xffffffffu, z_h, rl);
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                uint32_t y[4] = {__byte_perm(wd[2 * c], 0x64646464u, 0x4140),
-                                 __byte_perm(wd[2 * c], 0x64646464u, 0x4342),
-                                 __byte_perm(wd[2 * c + 1], 0x64646464u, 0x4140),
-                                 __byte_perm(wd[2 * c + 1], 0x64646464u, 0x4342)};
+            for (int v = 0; v < kVec; ++v) {
+              const int group = dim_of(v) / GROUP;
+              const uint32_t s_w = kS == 2 && (group & 2) ? sw[kS - 1] : sw[0];
+              const uint32_t z = zw >> (8 * group) & 0xFFu;
+              const uint32_t s2 = __byte_perm(s_w, 0, group & 1 ? 0x3232 : 0x1010);
+              const uint32_t z2 = (0x6400u + z) * 0x00010001u;            // 1024 + z, exact
+              const uint4 w4 = *reinterpret_cast<const uint4*>(src + (k * kVec + v) * 512);
+              uint32_t wd[4] = {w4.x, w4.y, w4.z, w4.w};
+              // this piece's image: chunks of eight dims from chunk c0 of its 64-dim half
+              uint8_t* dst = tile + (dim_of(v) >> 6) * (kTok * 128) + row * 128;
+              const uint32_t c0 = (dim_of(v) & 63) >> 3;
+              if constexpr (BITS == 4) {
+                // lanes t and t + 2 store to different halves, of the same banks: they take their
+                // four chunks in another order, so the eight lanes of a store meet all the banks
+                const uint32_t flip = D == 128 ? (t & 2) : 0;
+                if (D == 128 && flip) {
+                  uint32_t x = wd[0]; wd[0] = wd[2]; wd[2] = x;
+                  x = wd[1]; wd[1] = wd[3]; wd[3] = x;
+                }
+                const uint32_t s16 = hmul2(s2, 0x2C002C00u);              // s / 16
+                auto scaled = [&](uint32_t x, uint32_t s) { return plain.value ? x : hmul2(x, s); };
+                const uint32_t z16 = (0x6400u + 16 * z) * 0x00010001u;    // 1024 + 16 z
 #pragma unroll
-                for (int x = 0; x < 4; ++x) y[x] = mul2(sub2(y[x], z2), s2);
-                *reinterpret_cast<uint4*>(dst + (((c0 + c) ^ (row & 7)) << 4)) =
-                    make_uint4(y[0], y[1], y[2], y[3]);
+                for (int c = 0; c < 4; ++c) {
+                  const uint32_t x = wd[c], x8 = x >> 8;
+                  const uint4 y = make_uint4(
+                      scaled(sub2((x & 0x000F000Fu) | 0x64006400u, z2), s2),       // codes 0, 4
+                      scaled(sub2((x & 0x00F000F0u) | 0x64006400u, z16), s16),     // 1, 5, times 16
+                      scaled(sub2((x8 & 0x000F000Fu) | 0x64006400u, z2), s2),      // 2, 6
+                      scaled(sub2((x8 & 0x00F000F0u) | 0x64006400u, z16), s16));   // 3, 7
+                  *reinterpret_cast<uint4*>(dst + (((c0 + (c ^ flip)) ^ (row & 7)) << 4)) = y;
+                }
+              } else {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  uint32_t y[4] = {__byte_perm(wd[2 * c], 0x64646464u, 0x4140),
+                                   __byte_perm(wd[2 * c], 0x64646464u, 0x4342),
+                                   __byte_perm(wd[2 * c + 1], 0x64646464u, 0x4140),
+                                   __byte_perm(wd[2 * c + 1], 0x64646464u, 0x4342)};
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    y[x] = sub2(y[x], z2);
+                    if constexpr (!plain.value) y[x] = hmul2(y[x], s2);
+                  }
+                  *reinterpret_cast<uint4*>(dst + (((c0 + c) ^ (row & 7)) << 4)) =
+                      make_uint4(y[0], y[1], y[2], y[3]);
+                }
               }
             }
           }
-        }
+        };
+        if (G == 1 && h == 0) unpack(std::integral_constant<bool, G == 1>{});
+        else unpack(std::false_type{});
         fence_proxy_async_smem();
         mbar_arrive(h == 0 ? &k_full[b] : &v_full[b]);
         // the slot is free (its lane has read it): the codes of a step to come
@@ -696,92 +849,96 @@ cache_prefix_kernel(const Prefix a) {
       for (int k = 0; k < SM::kAhead; ++k) rows[k] = rows[k + 1];
     }
     cp_wait<0>();
-  } else if (warp == kMmaWarp) {
-    // ---- products: the whole warp runs the loop, so that descriptors stay in uniform registers;
-    // one lane issues ----
-    constexpr uint32_t id_qk = make_idesc(/*f16*/ 0, 0, 0, 128, kTok);
-    constexpr uint32_t id_pv = make_idesc(/*f16*/ 0, 0, /*B MN-major*/ 1, 128, D);
-    const bool elected = elect_one();
-    // operand tiles are 1024-byte aligned: an offset in 16-byte units adds to a descriptor
-    const uint64_t q_desc = smem_desc(smem_u32(q_tile(0)), 16, 1024, kSwizzle128B);
-    const uint64_t k_desc = smem_desc(smem_u32(k_tile(0)), 16, 1024, kSwizzle128B);
-    const uint64_t v_desc = smem_desc(smem_u32(v_tile(0)), kTok * 128, 1024, kSwizzle128B);
-    uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_pv[2] = {0, 0};
-    uint32_t g_base = 0;
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, &abort_flag, info));
-      return ok;
-    };
-    for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
-      const Unit w = get_unit(a, u);
-      auto qk = [&](int i, int s) {
-        const uint32_t gs = g_base + s;
-        const int b = gs & 1;
-        if (!wait(&k_full[b], (gs >> 1) & 1u)) return;
-        tc_fence_after();
-        if (elected) {
-          const uint64_t qd = q_desc + (w.two && i ? kTile / 16 : 0), kd = k_desc + b * (kTile / 16);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t at = ((kk >> 2) * (kTok * 128) + (kk & 3) * 32) / 16;
-            tc_mma_f16(tm_s(i), qd + at, kd + at, id_qk, kk ? 1u : 0u);
-          }
-          tc_commit(&s_full[i]);
-          if (!w.two || i == 1) tc_commit(&k_empty[b]);
-        }
-        __syncwarp();
+  } else {
+    registers_down<kMmaRegs>();      // (in this branch: code that others reach keeps its registers)
+    if (warp == kMmaWarp) {
+      // ---- products: the whole warp runs the loop, so that descriptors stay in uniform registers;
+      // one lane issues ----
+      constexpr uint32_t id_qk = make_idesc(/*f16*/ 0, 0, 0, 128, kTok);
+      constexpr uint32_t id_pv = make_idesc(/*f16*/ 0, 0, /*B MN-major*/ 1, 128, D);
+      const bool elected = elect_one();
+      // operand tiles are 1024-byte aligned: an offset in 16-byte units adds to a descriptor
+      const uint64_t q_desc = smem_desc(smem_u32(q_tile(0)), 16, 1024, kSwizzle128B);
+      const uint64_t k_desc = smem_desc(smem_u32(k_tile(0)), 16, 1024, kSwizzle128B);
+      const uint64_t v_desc = smem_desc(smem_u32(v_tile(0)), kTok * 128, 1024, kSwizzle128B);
+      uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_pv[2] = {0, 0};
+      uint32_t g_base = 0;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, info));
+        return ok;
       };
-      if (!wait(&q_full[0], n_q[0] & 1)) break;
-      ++n_q[0];
-      if (w.two) {
-        if (!wait(&q_full[1], n_q[1] & 1)) break;
-        ++n_q[1];
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (steps_of(w, i) == 0) continue;
-        // S takes the place of the last unit's weights
-        if (n_pv[i] > 0 && !wait(&pv_done[i], (n_pv[i] - 1) & 1)) break;
-        qk(i, step_of(w, i, 0));
-      }
-      const int most = steps_of(w, 0);
-      for (int r = 0; r < most && ok; ++r) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (!ok || r >= steps_of(w, i)) continue;
-          const uint32_t gs = g_base + step_of(w, i, r);
+      for (int u = blockIdx.x; ok && u < a.units; u += gridDim.x) {
+        const Unit w = get_unit(a, u);
+        auto qk = [&](int i, int s) {
+          const uint32_t gs = g_base + s;
           const int b = gs & 1;
-          if (!wait(&p_full[i], n_p[i] & 1)) break;
-          ++n_p[i];
-          if (!wait(&v_full[b], (gs >> 1) & 1u)) break;
+          if (!wait(&k_full[b], (gs >> 1) & 1u)) return;
           tc_fence_after();
           if (elected) {
-            const uint64_t vd = v_desc + b * (kTile / 16);
+            const uint64_t qd = q_desc + (w.two && i ? kTile / 16 : 0);
+            const uint64_t kd = k_desc + b * (kTile / 16);
 #pragma unroll
-            for (int kk = 0; kk < kTok / 16; ++kk)
-              tc_mma_f16_ts(tm_o(i), tm_s(i) + (kk >> 2) * 64 + (kk & 3) * 8, vd + kk * (2048 / 16),
-                            id_pv,
-                            (r | kk) ? 1u : 0u);
-            tc_commit(&pv_done[i]);
-            if (!w.two || i == 1) tc_commit(&v_empty[b]);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t at = ((kk >> 2) * (kTok * 128) + (kk & 3) * 32) / 16;
+              tc_mma_f16(tm_s(i), qd + at, kd + at, id_qk, kk ? 1u : 0u);
+            }
+            tc_commit(&s_full[i]);
+            if (!w.two || i == 1) tc_commit(&k_empty[b]);
           }
           __syncwarp();
-          ++n_pv[i];
-          if (r + 1 < steps_of(w, i)) {
-            // the next S takes the place of the weights that this product reads
-            if (!wait(&pv_done[i], (n_pv[i] - 1) & 1)) break;
-            qk(i, step_of(w, i, r + 1));
+        };
+        if (!wait(&q_full[0], n_q[0] & 1)) break;
+        ++n_q[0];
+        if (w.two) {
+          if (!wait(&q_full[1], n_q[1] & 1)) break;
+          ++n_q[1];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (steps_of(w, i) == 0) continue;
+          // S takes the place of the last unit's weights
+          if (n_pv[i] > 0 && !wait(&pv_done[i], (n_pv[i] - 1) & 1)) break;
+          qk(i, step_of(w, i, 0));
+        }
+        const int most = steps_of(w, 0);
+        for (int r = 0; r < most && ok; ++r) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (!ok || r >= steps_of(w, i)) continue;
+            const uint32_t gs = g_base + step_of(w, i, r);
+            const int b = gs & 1;
+            if (!wait(&p_full[i], n_p[i] & 1)) break;
+            ++n_p[i];
+            if (!wait(&v_full[b], (gs >> 1) & 1u)) break;
+            tc_fence_after();
+            if (elected) {
+              const uint64_t vd = v_desc + b * (kTile / 16);
+#pragma unroll
+              for (int kk = 0; kk < kTok / 16; ++kk)
+                tc_mma_f16_ts(tm_o(i), tm_s(i) + (kk >> 2) * 64 + (kk & 3) * 8, vd + kk * (2048 / 16),
+                              id_pv,
+                              (r | kk) ? 1u : 0u);
+              tc_commit(&pv_done[i]);
+              if (!w.two || i == 1) tc_commit(&v_empty[b]);
+            }
+            __syncwarp();
+            ++n_pv[i];
+            if (r + 1 < steps_of(w, i)) {
+              // the next S takes the place of the weights that this product reads
+              if (!wait(&pv_done[i], (n_pv[i] - 1) & 1)) break;
+              qk(i, step_of(w, i, r + 1));
+            }
           }
         }
+        g_base += w.steps;
       }
-      g_base += w.steps;
+      if (elected) {
+        tc_commit(&sh.mma_done);           // let what was issued finish, after an error too
+        mbar_drain_bounded(&sh.mma_done, 0);
+      }
+      __syncwarp();
     }
-    if (elected) {
-      tc_commit(&mma_done);           // let what was issued finish, after an error too
-      mbar_drain_bounded(&mma_done, 0);
-    }
-    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -902,8 +1059,6 @@ gptq_status run_cache_prefix(const CacheView& c, const CacheRows& r, int dim, in
                              int32_t* info, cudaStream_t stream) {
   Prefix a{};
   a.cache = c;
-  a.cache.width =
-      static_cast<int>((q.prefix_len + (static_cast<int64_t>(1) << c.page_shift) - 1) >> c.page_shift);
   a.table = q.prefix_table;
   a.len = q.prefix_len;
   a.q = q.q;

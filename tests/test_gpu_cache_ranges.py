@@ -31,7 +31,7 @@ def _queries(n, dim, seed):
 
 def _attend(host, tokens, q, scale=None, rows=None):
     """Every row of q [rows, 1, dim] meets the first `tokens` positions: as the query heads of one
-    token, and as a shared prefix."""
+    token, and as a shared prefix (from 33 rows on by the kernel for many rows)."""
     scale = host.dim ** -0.5 if scale is None else scale
     pages = host.part["k"][0].shape[0]
     table = np.arange(pages, dtype=np.int32)
@@ -45,10 +45,11 @@ def _attend(host, tokens, q, scale=None, rows=None):
     assert int(cache.info.item()) == 0
     args = [p[:, 0].reshape(-1, p.shape[-1])[:tokens] for half in "kv" for p in host.part[half]]
     for i in range(n) if rows is None else rows:
-        for got, shared in ((own[0, i], False), (pre[i, 0], True)):
-            ref, tol = oracle.attend_bound(q[i, 0].double().numpy(), *args, scale)
+        for got, many in ((own[0, i], False), (pre[i, 0], n > 32)):
+            ref, tol = oracle.attend_bound(q[i, 0].double().numpy(), *args, scale,
+                                           many_rows=many)
             err = np.abs(got.double().cpu().numpy() - ref)
-            assert np.all(err <= tol), (i, shared, float((err / tol).max()), int((err > tol).sum()))
+            assert np.all(err <= tol), (i, many, float((err / tol).max()), int((err > tol).sum()))
 
 
 FORMATS = [(128, 4, 128), (128, 8, 128), (128, 4, 32), (128, 8, 64), (64, 4, 64), (64, 8, 32)]
@@ -122,6 +123,82 @@ def test_queries_and_keys_of_opposite_size(dim, bits, group, n, up):
     q = (_queries(n, dim, 3).float() * 2.0 ** (up - 2)).to(torch.bfloat16)
     assert torch.isfinite(q).all()
     _attend(host, 90, q)
+
+
+# ------------------------------------------------------------------------------------------------
+# a prefix that many rows meet
+# ------------------------------------------------------------------------------------------------
+ROWS = (0, 17, 39, 139)
+
+
+@pytest.mark.parametrize("dim,bits,group", FORMATS)
+@pytest.mark.parametrize("n", [40, 140])
+@pytest.mark.parametrize("outliers,kx,qx", [(0, 1, 1), (2, 15, 8), (4, 20, 20)])
+def test_prefix_keys_with_outlier_channels(dim, bits, group, n, outliers, kx, qx):
+    """A few channels far above the others, in keys and queries: the scores' error must not grow
+    with the scores (with one grid a row; several are fp16 images). Six tokens stand out and share the weight, so an error of their scores shows."""
+    rng = np.random.default_rng(8)
+    k, v = (rng.standard_normal((600, dim)).astype(np.float32) for _ in range(2))
+    at = rng.permutation(dim)[:outliers]
+    k[:, at] *= kx / 4
+    k[np.ix_(range(50, 590, 100), at)] = kx
+    q = _queries(n, dim, 9).float()
+    q[:, 0, at] = qx
+    _attend(_host(k, v, bits, group), 600, q.to(torch.bfloat16), rows=[r for r in ROWS if r < n])
+
+
+@pytest.mark.parametrize("dim,bits,group", FORMATS)
+@pytest.mark.parametrize("n", [40, 140])
+@pytest.mark.parametrize("up", [20, 40, 70])
+def test_prefix_of_one_large_value_without_weight(dim, bits, group, n, up):
+    """An early token with a huge value that no row gives any weight, and one with a small value:
+    the others' values are kept as well as without them."""
+    rng = np.random.default_rng(10)
+    k, v = (rng.standard_normal((600, dim)).astype(np.float32) for _ in range(2))
+    q = _queries(n, dim, 11).float()
+    q[:, 0, 3] = 6.0
+    k[5], v[5] = 0, v[5] * np.float32(2.0 ** up)
+    k[5, 3] = -60 * dim ** 0.5 - up             # its weight: e^-6(60 + up / dim^0.5)
+    v[400] *= np.float32(2.0 ** -up)
+    _attend(_host(k, v, bits, group), 600, q.to(torch.bfloat16), rows=[r for r in ROWS if r < n])
+
+
+@pytest.mark.parametrize("dim,bits,group", FORMATS)
+@pytest.mark.parametrize("n", [40, 140])
+@pytest.mark.parametrize("size", [1e-4, 1e-8])
+def test_prefix_tokens_whose_values_are_zero(dim, bits, group, n, size):
+    rng = np.random.default_rng(12)
+    k, v = (rng.standard_normal((500, dim)).astype(np.float32) for _ in range(2))
+    v *= np.float32(size)
+    v[rng.random(500) < 0.33] = 0
+    v[37, group // 2:] = 0
+    if group < dim:
+        v[:, :group] = 0                  # a head dimension padded up
+    host = _host(k, v, bits, group)
+    _attend(host, 500, _queries(n, dim, 13), rows=[r for r in ROWS if r < n])
+
+
+@pytest.mark.parametrize("dim,bits,group", FORMATS)
+@pytest.mark.parametrize("n", [40, 140])
+@pytest.mark.parametrize("small,large", [(-40, 40), (-60, 70)])
+def test_prefix_value_scales_far_apart(dim, bits, group, n, small, large):
+    rng = np.random.default_rng(14)
+    k, v = (rng.standard_normal((600, dim)).astype(np.float32) for _ in range(2))
+    e = np.where((np.arange(600) // 128) % 2 == 1, large, small) + rng.integers(-9, 9, 600)
+    host = _host(k, v * np.exp2(e.astype(np.float32))[:, None], bits, group)
+    rows = [r for r in ROWS if r < n]
+    _attend(host, 600, torch.zeros(n, 1, dim, dtype=torch.bfloat16), rows=rows)
+    _attend(host, 600, _queries(n, dim, 15), rows=rows)
+
+
+@pytest.mark.parametrize("dim,bits,group", FORMATS)
+@pytest.mark.parametrize("up", [124, 100, -110])
+def test_prefix_queries_and_keys_of_opposite_size(dim, bits, group, up):
+    rng = np.random.default_rng(16)
+    k, v = (rng.standard_normal((300, dim)).astype(np.float32) for _ in range(2))
+    host = _host(k * np.float32(2.0 ** (2 - up)), v, bits, group)
+    q = (_queries(40, dim, 17).float() * 2.0 ** (up - 2)).to(torch.bfloat16)
+    _attend(host, 300, q, rows=[0, 17, 39])
 
 
 # ------------------------------------------------------------------------------------------------
