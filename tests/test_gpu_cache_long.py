@@ -1,6 +1,6 @@
 """Attention whose work gives every part of the kernels several rounds: warps that go over many steps
-of a ring, runs of many tiles and their joins. The shapes are checked against the device, so that
-they keep reaching those paths."""
+of a ring, runs of many tiles and their joins, and units of the prefix kernel that follow one another
+on a CTA. The shapes are checked against the device, so that they keep reaching those paths."""
 import numpy as np
 import pytest
 import torch
@@ -132,3 +132,80 @@ def test_an_item_per_warp_of_many_steps(dim, bits, group):
     assert int(cache.info.item()) == 0 and torch.all(out[300] == 0)
     for b, qh, parts in want:
         _check(out[b, qh], q[b, qh], parts, dim ** -0.5)
+
+
+# ------------------------------------------------------------------------------------------------
+# units of the prefix kernel
+# ------------------------------------------------------------------------------------------------
+def _units(heads, rows, prefix):
+    """(units, steps of the longest) of the prefix kernel: per item of up to 256 rows the split with
+    the fewest rounds times their length."""
+    sms, tiles = _sms(), -(-prefix // 128)
+    items = heads * -(-rows // 256)
+    most = min(tiles, max(max(items, 2 * sms) // items, 1))
+    cost = {s: -(-items * s // sms) * (-(-tiles // s) + 2) for s in range(1, most + 1)}
+    s = min(cost, key=lambda k: (cost[k], k))
+    return items * s, -(-tiles // s)
+
+
+def _prefix_case(heads, n, ratio, prefix, dim, bits, group, picks, scales=False, page=128):
+    pages = -(-prefix // page)
+    host = HostCache(pages, heads, page, dim, bits, group, seed=heads + n)
+    if scales:          # V's grids rise and fall from tile to tile
+        e = np.array([0, 11, -12, 3, 14, -10, 12, 0, -14, 5])[np.arange(pages * page) // 128 % 10]
+        host.part["v"][1][:] *= np.exp2(e).astype(np.float32).reshape(pages, 1, page, 1)
+    ptable = np.random.default_rng(n).permutation(pages).astype(np.int32)
+    if scales:
+        ptable = np.arange(pages, dtype=np.int32)
+    tables = np.repeat(ptable[None], n, 0)
+    q, want = _aimed_rows(host, tables, np.full(n, prefix), ratio, picks)
+    cache = host.device()
+    args = (q.to(DEV), dev(ptable), prefix, dev(np.zeros((n, 1), np.int32)),
+            dev(np.zeros(n, np.int32)))
+    out = cache.attend_shared(*args)
+    again = cache.attend_shared(*args)
+    torch.cuda.synchronize()
+    assert int(cache.info.item()) == 0 and torch.equal(out, again)
+    for i, qh, parts in want:
+        _check(out[i, qh], q[i, qh], parts, dim ** -0.5, many_rows=True)
+
+
+@pytest.mark.parametrize("dim,bits,group", FORMATS)
+@pytest.mark.parametrize("scales", [False, True])
+def test_units_of_two_and_one_row_tiles_on_one_cta(dim, bits, group, scales):
+    """192 items of 32 heads, the last of each head with 20 rows: CTAs that take a second unit, of
+    the other kind too."""
+    heads, n, prefix = 32, 260, 700
+    units, steps = _units(heads, n * 5, prefix)
+    assert units > _sms() and steps >= 5
+    rng = np.random.default_rng(6)
+    picks = [(i, int(rng.integers(0, heads)) * 5 + r, at) for i, r, at in (
+        (0, 0, 0), (51, 0, 699), (51, 1, 128), (51, 2, 127), (102, 3, 383), (255, 4, 600),
+        (256, 0, 512), (259, 4, 640), (258, 2, 1), (130, 1, 300))]
+    picks += [(257, 31 * 5, 699), (256, 31 * 5 + 1, 5), (0, 31 * 5 + 2, 511), (140, 30 * 5, 256)]
+    _prefix_case(heads, n, 5, prefix, dim, bits, group, picks, scales)
+
+
+@pytest.mark.parametrize("heads,prefix", [(100, 640), (100, 700), (150, 1150), (74, 2500)])
+@pytest.mark.parametrize("n,scales", [(40, False), (128, True)])
+def test_units_of_one_row_tile(heads, prefix, n, scales):
+    """Items near the number of SMs, at most 128 rows: both softmax groups over every other tile,
+    for odd and even counts."""
+    units, steps = _units(heads, n, prefix)
+    assert steps >= 5
+    rng = np.random.default_rng(7)
+    picks = [(int(rng.integers(0, n)), int(rng.integers(0, heads)), at) for at in
+             (0, 127, 128, 255, 256, 511, 512, 639, prefix - 1, prefix - 130)]
+    dim, bits, group = ((64, 8, 32), (64, 4, 64))[scales]
+    _prefix_case(heads, n, 1, prefix, dim, bits, group, picks, scales)
+
+
+@pytest.mark.parametrize("dim,bits,group", [(128, 4, 128), (128, 8, 32)])
+def test_units_of_many_steps(dim, bits, group):
+    """A prefix of more than 20 tiles a unit, grids that rise and fall."""
+    heads, n, prefix = 20, 300, 22 * 128 * 7 + 77
+    units, steps = _units(heads, n, prefix)
+    assert steps >= 20
+    picks = [(i, qh, at) for i, qh, at in ((0, 0, 128 * 21), (255, 7, 128 * 22 + 1), (256, 19, 77),
+                                           (299, 3, prefix - 1), (130, 12, 128 * 44), (7, 9, 5000))]
+    _prefix_case(heads, n, 1, prefix, dim, bits, group, picks, scales=True)
