@@ -223,7 +223,8 @@ class QuantizedCache:
     of sequence b, the very last one at lengths[b] - 1; without starts, row b is the last position
     of sequence b. A step appends with the lengths after it and attends with the same ones. The
     index tensors are read on the device, so a captured step can be replayed with new values in
-    them; rows behind starts[batch] are ignored.
+    them; rows behind starts[batch] are ignored: outputs of theirs that are given stay as they are,
+    and are undefined in a tensor that the call allocates.
 
     Calls run on `stream` (default: the current stream of the cache's device) and allocate their
     workspace there. `info` is the device status word: nonzero once a call met a position without

@@ -132,8 +132,8 @@ gptq_status run_cache_append(const CacheView& c, const CacheRows& r, int dim, in
 gptq_status run_cache_read(const CacheView& c, const CacheRows& r, int dim, int bits, int group,
                            void* K_out, void* V_out, bool bf16, int32_t* info, cudaStream_t stream);
 
-// Attention over the cache. prefix_len < 0: plain; else rows also meet positions 0 .. prefix_len - 1
-// of the common sequence behind prefix_table.
+// Attention over the cache. With prefix_len > 0 rows also meet positions 0 .. prefix_len - 1 of the
+// common sequence behind prefix_table; 0: plain.
 struct CacheQuery {
   const __nv_bfloat16* q;   // [n][ldq], heads * ratio vectors a row
   int64_t ldq;

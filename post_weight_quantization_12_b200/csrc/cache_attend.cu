@@ -107,9 +107,9 @@ struct Level {
   int64_t ldo;
   float* mid;                   // [n][heads ratio][D] fp32 results of the level before, and its lse
   float* mid_lse;               // read if `out` is set and they are not null
-  float* part;                  // [2 grid][R][D], partial results
-  float* part_lse;              // [2 grid][R]
-  int32_t* join;                // [grid][8]: what the run's last item needs joined
+  float* part;                  // [2 runs][R][D], partial results
+  float* part_lse;              // [2 runs][R]
+  int32_t* join;                // [runs][8]: what the run's last item needs joined
   int32_t* info;
 };
 
@@ -434,6 +434,7 @@ cache_attend_kernel(const Level a) {
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
+  // (the trigger stays behind the wait: cache_prefix_kernel may follow, and does not wait itself)
   griddep_wait();
   griddep_launch_dependents();
   const Cut cut = find_tile<R, kTile, C::kWorkers>(a, find);
@@ -528,7 +529,7 @@ cache_attend_kernel(const Level a) {
     const int limit_lo = limit_of(row_first);
     const int limit_hi = limit_of(min(row_first + R, n_rows) - 1);
 
-    // ---- this warp's steps: tokens first + 64 i, and the pages of 32 of them, one per lane ----
+    // ---- this warp's steps: tokens first + kTile i, and the pages of 32 of them, one per lane ----
     const int stop = static_cast<int>(
         min(static_cast<int64_t>(limit_hi), (static_cast<int64_t>(tile0) + run) * kTile));
     const int first = tok_begin + kStep * wi;
@@ -1057,6 +1058,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 cache_join_kernel(const Level a) {
   __shared__ float sh[kJoinWarps][D];
   __shared__ float sh_m[kJoinWarps], sh_l[kJoinWarps];
+  // (the trigger stays behind the wait: cache_prefix_kernel may follow, and does not wait itself)
   griddep_wait();
   griddep_launch_dependents();
   const int64_t c = blockIdx.x;
@@ -1067,11 +1069,10 @@ cache_join_kernel(const Level a) {
   const int64_t row0 = __ldcg(join + 4);
   const int row_first = __ldcg(join + 5);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int rows_here = R;
   constexpr int per_row = kJoinWarps / R < 1 ? 1 : kJoinWarps / R;     // warps of a row
   constexpr int kVec = D / 32;                            // dims of a lane: 2 or 4
-  for (int rr = warp / per_row; rr < rows_here; rr += kJoinWarps / per_row) {
-    const int r = rr, sub = warp % per_row;
+  for (int r = warp / per_row; r < R; r += kJoinWarps / per_row) {
+    const int sub = warp % per_row;
     float m = kNegInf, l = 0.f, acc[kVec];
 #pragma unroll
     for (int k = 0; k < kVec; ++k) acc[k] = 0.f;
@@ -1106,7 +1107,7 @@ cache_join_kernel(const Level a) {
       }
     }
     if (per_row > 1) {
-      // the loop runs once for every warp here: rows_here * per_row == kJoinWarps
+      // the loop runs once for every warp here: R * per_row == kJoinWarps
 #pragma unroll
       for (int k = 0; k < kVec; ++k) sh[warp][lane * kVec + k] = acc[k];
       if (lane == 0) {

@@ -209,8 +209,11 @@ __device__ __forceinline__ bool named_barrier_or(uint32_t id, uint32_t nthreads,
 
 // Programmatic dependent launch: kernels of this library are launched so that they may start
 // while the kernel before them in the stream finishes. griddep_wait() returns once that kernel
-// has completed and its memory is visible; every kernel calls it before its first global memory
-// access. griddep_launch_dependents() lets the next kernel be scheduled now (it still waits).
+// has completed and its memory is visible; a kernel calls it before its first global memory access.
+// griddep_launch_dependents() lets the next kernel be scheduled now (it still waits).
+// One exception: cache_prefix_kernel waits at its end. It reads and writes nothing that the kernel in
+// front of it writes, and that kernel (the attention or the join kernel of cache_attend.cu) triggers
+// only after its own wait, so all that came before it is complete by then.
 __device__ __forceinline__ void griddep_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -125,7 +125,8 @@ gptq_status set_max_dynamic_smem(const void* kernel, int bytes);
 void count_launch(uint64_t n = 1);
 
 // Launch with programmatic stream serialization: the kernel may begin while the previous kernel
-// in the stream drains; it must call griddep_wait() before touching global memory. Counts the
+// in the stream drains; it must call griddep_wait() before touching global memory (common.cuh names
+// the one kernel that need not, and what that rests on). Counts the
 // launch and reports launch errors.
 template <typename... KArgs, typename... Args>
 inline gptq_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
