@@ -486,9 +486,8 @@ gptq_status gptq_cache_attend(const gptq_cache* cache, const gptq_cache_rows* ro
  *   ws_dev          gptq_cache_workspace_size(cache, n, ratio, 1) bytes.
  * Arithmetic of the prefix for more than 32 rows (n * ratio): its values become fp16 before the
  * product (2^-12 of each, or 2^-32 of the largest of the 32 tokens around it, their own where scales
- * lie 2^13 and more apart), and where a row has several grids (group < dim) its keys, too, which
- * moves a score by up to 2^-12 of scale * sum |q k|. With one grid a row the keys' codes are exact, as
- * in gptq_cache_attend. V scales below 2^-96 lose accuracy. Other arguments, arithmetic and
+ * lie 2^13 and more apart; V scales below 2^-96 lose accuracy). Its keys are exact, or where a row has
+ * several grids (group < dim) off by 2^-32 of the largest of 32 tokens. Other arguments, arithmetic and
  * errors as gptq_cache_attend.
  */
 gptq_status gptq_cache_attend_shared(const gptq_cache* cache, const gptq_cache_rows* rows,

@@ -104,7 +104,7 @@ def attend_bound(q, kc, ks, kz, vc, vs, vz, scale: float, image16: bool = False,
       groups of a token. With `many_rows` (a shared prefix's own kernel) the values are images, off
       by 2^-12 of themselves or 2^-32 of the largest of their 32 tokens (their own where that one is
       2^13 and more above them), which the unit goes by, too; and where a row has several grids the
-      keys are images likewise.
+      keys are sums of two images, off by 2^-32 of the largest of their 32 tokens.
     * The sum over tokens runs in steps of 16 and is joined from parts: (tokens / 16 + 64) 2^-22 of
       sum p |v|. Each step adds codes and takes zero points out: 2^-22 of sum p s (code + z) more.
       A code enters as an fp16 subnormal, which the tensor core aligns as if it were 2^-14, that is
@@ -154,7 +154,7 @@ def attend_bound(q, kc, ks, kz, vc, vs, vz, scale: float, image16: bool = False,
         if many_rows:
             if G > 1:
                 tops = np.pad(np.abs(k).max(1), (0, -T % 32)).reshape(-1, 32).max(1).repeat(32)[:T]
-                e += 2.0 ** -12 * kq + 2.0 ** -32 * scale * tops * np.abs(q).sum()
+                e += 2.0 ** -32 * scale * tops * np.abs(q).sum()
             bound = (p * e) @ np.abs(v - out) * (1 + 2 * (p * e).sum() + e[p > 2.0 ** -20].max())
         else:
             bound = 2 * e.max() * mass

@@ -9,10 +9,13 @@
 // K: where a row has one grid, its image is q - z, exact, and the score is x = S times the token's
 // scale, which the softmax groups read from shared memory: a rounding of the keys' images would move
 // a score by 2^-12 of sum |q k|, which is more than the output's own rounding where a few channels of
-// the keys stand out. Where a row has several grids no factor can be taken out: the image is
-// s' (q - z), one rounding (2^-12), s' = s 2^(T - E) with E the largest exponent among the scales of
-// 32 tokens, so that the largest image stays below 65504.
-// V: an image of that kind throughout, whose error stays 2^-12 of the value. Its power of two e goes
+// the keys stand out. Where a row has several grids no factor can be taken out: s' (q - z) needs up
+// to 16 bits and becomes the sum of two fp16 numbers, the rounded one and what it left, in two images
+// and twice the products (one buffer instead of two then: 128 rows x 8 heads x 4 over 32,768 tokens
+// of 4-bit codes, group 32, 192 us, and 159 with one image; 96 rows x 32 heads over 8192 tokens 160
+// and 153). s' = s 2^(T - E), E the largest exponent among the scales of 32 tokens, so that the
+// largest image stays below 65504.
+// V: the rounded image alone, throughout; its error stays 2^-12 of the value. Its power of two e goes
 // into the exponent of P, per 32 tokens, and per token where scales lie further apart, so a value far
 // above the others takes no bits of theirs unless the row gives it weight. Groups whose values are
 // all zero, whose grid is [-1, 1], do not count for E.
@@ -63,6 +66,8 @@ constexpr float kNegInf = -INFINITY;
 // otherwise (first case below: 153 us without, 148 with; 88 registers with less for unpacking 151).
 constexpr int kLaunchRegs = 72, kMmaRegs = 40, kSoftmaxRegs = 80;
 static_assert(kMmaRegs + 4 * kSoftmaxRegs + 2 * kLaunchRegs <= 7 * kLaunchRegs);
+
+enum Image { kPlainImage, kOneImage, kTwoImages };      // see the unpacking
 
 struct Prefix {
   CacheView cache;
@@ -199,6 +204,11 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
 __device__ __forceinline__ float pow2(int e) {          // e in [-126, 127]
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
@@ -237,6 +247,10 @@ cache_prefix_kernel(const Prefix a) {
   constexpr int kTile = SM::kTileBytes;
   // exponent of the largest scale in a token's images: below 2^(kTop + 1) (2^BITS - 1) < 65504
   constexpr int kTop = BITS == 4 ? 11 : 7;
+  // K's tiles: two buffers of images, or one of two images that add up to the values
+  constexpr bool kPair = G > 1;
+  auto k_buffer = [](uint32_t gs) -> int { return kPair ? 0 : gs & 1; };
+  auto k_phase = [](uint32_t gs) -> uint32_t { return kPair ? gs & 1u : (gs >> 1) & 1u; };
   extern __shared__ __align__(1024) uint8_t smem[];    // (operand tiles: multiples of 1024 bytes)
   auto q_tile = [&](int i) { return smem + i * kTile; };
   auto k_tile = [&](int b) { return smem + (2 + b) * kTile; };
@@ -701,12 +715,14 @@ cache_prefix_kernel(const Prefix a) {
       {
         cp_wait<SM::kAhead - 1>();
         __syncwarp();
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(h == 0 ? &k_empty[b] : &v_empty[b], ph ^ 1u,
-                                                       abort_flag, info));
+        ok = __all_sync(0xffffffffu,
+                        h == 0 ? mbar_wait_bounded(&k_empty[k_buffer(gs)], k_phase(gs) ^ 1u,
+                                                   abort_flag, info)
+                               : mbar_wait_bounded(&v_empty[b], ph ^ 1u, abort_flag, info));
         if (!ok) break;
         const uint8_t* warp_codes = code_slot(cb, h) + dw * (SM::kCodeBytes / kDqWarps);
         const uint8_t* src = warp_codes + lane * 16;
-        uint8_t* tile = h == 0 ? k_tile(b) : v_tile(b);
+        uint8_t* tile = h == 0 ? k_tile(k_buffer(gs)) : v_tile(b);
         // A group of V without values has the grid [-1, 1], a scale that would push the others' out
         // of fp16's range: it counts as 0.
         if (h == 1) {
@@ -778,7 +794,17 @@ cache_prefix_kernel(const Prefix a) {
             r_h[k] = half2_bits(__uint_as_float(s_h[k] << 16) * unit,
                                 __uint_as_float(s_h[k] & 0xFFFF0000u) * unit);
         }
-        auto unpack = [&](auto plain) {            // plain: images without scales
+        // images without scales, with them, or with them and a second image of what their rounding
+        // left (exact: the residual of a product)
+        auto unpack = [&](auto kind) {
+          constexpr bool kScaled = kind.value != kPlainImage, kRest = kind.value == kTwoImages;
+          uint32_t rest[4];
+          auto image = [&](uint32_t x, uint32_t s, int i) -> uint32_t {
+            if constexpr (!kScaled) return x;
+            const uint32_t y = hmul2(x, s);
+            if constexpr (kRest) rest[i] = hfma2(x, s, y ^ 0x80008000u);
+            return y;
+          };
 #pragma unroll
           for (int k = 0; k < KI; ++k) {
             const int rl = k * RPI + g, row = dw * kDqRows + rl;
@@ -807,17 +833,20 @@ cache_prefix_kernel(const Prefix a) {
                   x = wd[1]; wd[1] = wd[3]; wd[3] = x;
                 }
                 const uint32_t s16 = hmul2(s2, 0x2C002C00u);              // s / 16
-                auto scaled = [&](uint32_t x, uint32_t s) { return plain.value ? x : hmul2(x, s); };
                 const uint32_t z16 = (0x6400u + 16 * z) * 0x00010001u;    // 1024 + 16 z
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                   const uint32_t x = wd[c], x8 = x >> 8;
                   const uint4 y = make_uint4(
-                      scaled(sub2((x & 0x000F000Fu) | 0x64006400u, z2), s2),       // codes 0, 4
-                      scaled(sub2((x & 0x00F000F0u) | 0x64006400u, z16), s16),     // 1, 5, times 16
-                      scaled(sub2((x8 & 0x000F000Fu) | 0x64006400u, z2), s2),      // 2, 6
-                      scaled(sub2((x8 & 0x00F000F0u) | 0x64006400u, z16), s16));   // 3, 7
-                  *reinterpret_cast<uint4*>(dst + (((c0 + (c ^ flip)) ^ (row & 7)) << 4)) = y;
+                      image(sub2((x & 0x000F000Fu) | 0x64006400u, z2), s2, 0),       // codes 0, 4
+                      image(sub2((x & 0x00F000F0u) | 0x64006400u, z16), s16, 1),     // 1, 5, times 16
+                      image(sub2((x8 & 0x000F000Fu) | 0x64006400u, z2), s2, 2),      // 2, 6
+                      image(sub2((x8 & 0x00F000F0u) | 0x64006400u, z16), s16, 3));   // 3, 7
+                  uint8_t* at = dst + (((c0 + (c ^ flip)) ^ (row & 7)) << 4);
+                  *reinterpret_cast<uint4*>(at) = y;
+                  if constexpr (kRest)
+                    *reinterpret_cast<uint4*>(at + kTile) =
+                        make_uint4(rest[0], rest[1], rest[2], rest[3]);
                 }
               } else {
 #pragma unroll
@@ -827,21 +856,21 @@ cache_prefix_kernel(const Prefix a) {
                                    __byte_perm(wd[2 * c + 1], 0x64646464u, 0x4140),
                                    __byte_perm(wd[2 * c + 1], 0x64646464u, 0x4342)};
 #pragma unroll
-                  for (int x = 0; x < 4; ++x) {
-                    y[x] = sub2(y[x], z2);
-                    if constexpr (!plain.value) y[x] = hmul2(y[x], s2);
-                  }
-                  *reinterpret_cast<uint4*>(dst + (((c0 + c) ^ (row & 7)) << 4)) =
-                      make_uint4(y[0], y[1], y[2], y[3]);
+                  for (int x = 0; x < 4; ++x) y[x] = image(sub2(y[x], z2), s2, x);
+                  uint8_t* at = dst + (((c0 + c) ^ (row & 7)) << 4);
+                  *reinterpret_cast<uint4*>(at) = make_uint4(y[0], y[1], y[2], y[3]);
+                  if constexpr (kRest)
+                    *reinterpret_cast<uint4*>(at + kTile) =
+                        make_uint4(rest[0], rest[1], rest[2], rest[3]);
                 }
               }
             }
           }
         };
-        if (G == 1 && h == 0) unpack(std::integral_constant<bool, G == 1>{});
-        else unpack(std::false_type{});
+        if (h == 0) unpack(std::integral_constant<int, kPair ? kTwoImages : kPlainImage>{});
+        else unpack(std::integral_constant<int, kOneImage>{});
         fence_proxy_async_smem();
-        mbar_arrive(h == 0 ? &k_full[b] : &v_full[b]);
+        mbar_arrive(h == 0 ? &k_full[k_buffer(gs)] : &v_full[b]);
         // the slot is free (its lane has read it): the codes of a step to come
         copy_codes(rows[SM::kAhead], cb);
       }
@@ -872,17 +901,19 @@ cache_prefix_kernel(const Prefix a) {
         const Unit w = get_unit(a, u);
         auto qk = [&](int i, int s) {
           const uint32_t gs = g_base + s;
-          const int b = gs & 1;
-          if (!wait(&k_full[b], (gs >> 1) & 1u)) return;
+          const int b = k_buffer(gs);
+          if (!wait(&k_full[b], k_phase(gs))) return;
           tc_fence_after();
           if (elected) {
             const uint64_t qd = q_desc + (w.two && i ? kTile / 16 : 0);
             const uint64_t kd = k_desc + b * (kTile / 16);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t at = ((kk >> 2) * (kTok * 128) + (kk & 3) * 32) / 16;
-              tc_mma_f16(tm_s(i), qd + at, kd + at, id_qk, kk ? 1u : 0u);
-            }
+            for (int x = 0; x < (kPair ? 2 : 1); ++x)
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t at = ((kk >> 2) * (kTok * 128) + (kk & 3) * 32) / 16;
+                tc_mma_f16(tm_s(i), qd + at, kd + x * (kTile / 16) + at, id_qk, x | kk ? 1u : 0u);
+              }
             tc_commit(&s_full[i]);
             if (!w.two || i == 1) tc_commit(&k_empty[b]);
           }

@@ -136,7 +136,7 @@ ROWS = (0, 17, 39, 139)
 @pytest.mark.parametrize("outliers,kx,qx", [(0, 1, 1), (2, 15, 8), (4, 20, 20)])
 def test_prefix_keys_with_outlier_channels(dim, bits, group, n, outliers, kx, qx):
     """A few channels far above the others, in keys and queries: the scores' error must not grow
-    with the scores (with one grid a row; several are fp16 images). Six tokens stand out and share the weight, so an error of their scores shows."""
+    with the scores. Six tokens stand out and share the weight, so an error of their scores shows."""
     rng = np.random.default_rng(8)
     k, v = (rng.standard_normal((600, dim)).astype(np.float32) for _ in range(2))
     at = rng.permutation(dim)[:outliers]
