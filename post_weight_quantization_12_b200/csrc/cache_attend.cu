@@ -30,14 +30,16 @@
 // What bounds it: HBM for 8-bit codes in long sequences (bits / 8 + 3 / group bytes a value); every
 // warp keeps three steps of 16 tokens (2 to 4 KB each) in flight through its own ring of 16-byte
 // copies of whole sectors (89 us for 131,072 tokens of 8-bit codes, 98 with each lane copying what
-// it consumes, at that stage of the kernel), four CTAs of four warps an SM. For 4-bit codes the integer pipe, which unpacks them, is as busy as the memory:
-// about 346 warp instructions a step of 16 tokens, 57 % of the issue slots and of that pipe.
+// it consumes, at that stage of the kernel), four CTAs of four warps an SM. For 4-bit codes the
+// integer pipe, which unpacks them, is as busy as the memory: about 346 warp instructions a step of
+// 16 tokens, 57 % of the issue slots and of that pipe.
 // Measured (128 dimensions, one grid a row, the whole call; fractions of the measured bandwidth):
-//   131,072 tokens, 8 heads of 8-bit codes, 4 query heads each    64 us, 0.65 (kernel 56.5); 6.1 TB/s
+//   131,072 tokens, 8 heads of 8-bit codes, 4 query heads each    64 us, 0.65 (kernel 56.6); 6.1 TB/s
 //     (0.93) in the steady state, the rest is start, last round and join
-//   32 sequences of 100 to 16,000 tokens, 8 heads of 4-bit codes  86 us, 0.49 (kernel 85.9); 4.0 TB/s
-//     (0.61) in the steady state
-//   one sequence of 37 tokens, 32 heads                           6 us on the device
+//   32 sequences of 100 to 16,000 tokens, 8 heads of 4-bit codes  89 us, 0.47 (kernel 89); 4.1 TB/s
+//     (0.62) in the steady state; with a second reference less (a denominator of operands over
+//     scales, and one reference for all groups, both wrong for scales far apart) 86
+//   one sequence of 37 tokens, 32 heads                           7 us on the device
 // Tried and slower: the products of the next step issued before this one's weights (4-bit codes 4.0
 // to 3.8 TB/s), two steps unrolled (90 to 92 us).
 #include <cuda_runtime.h>

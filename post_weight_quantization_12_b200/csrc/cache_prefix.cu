@@ -30,20 +30,25 @@
 //                    scheduler lets it go first, and every other role waits for it)
 //   warps 4-11, 12-19  softmax of row tile 0 and 1, two threads a row: each takes half of the
 //                    tokens, and half of the dimensions when they bring Q in and write the results
-//   warps 20-23, 24-27  unpack K and V of the next tiles into two buffers each, loads a tile ahead
+//   warps 20-23, 24-27  unpack K and V of the next tiles into two buffers each, loads a tile ahead;
+//                    those of V tell the softmax groups what the images lack
 // With no more than 128 rows in an item, both softmax groups take the same rows and every other
 // token tile. The runs' results (row, fp32, with its log-sum) are joined by cache_merge_kernel.
 //
 // What bounds it. Two row tiles: the chain of a step. Both products read operands from shared or
-// tensor memory (about 840 cycles of S, 700 of O a row tile and token tile), and with the hand-overs
-// between them a step of both row tiles takes about 4.4k cycles: 128 sequences x 8 heads of 4-bit
-// codes x 4 query heads, prefix 32,768, 130 us in all, 532 TFLOP/s (0.32 of the measured bf16 rate);
-// this kernel 87 us, tensor pipe 37 % busy. One row tile: unpacking, about 3.0k cycles a token tile:
-// 96 sequences x 32 heads of 8-bit codes, prefix 8192, 122 us in all, this kernel 47 us. The rest
-// of both is the sequences' own level, the merge (about 9 us) and what lies between them.
-// Tried and slower (first case): S in two halves of the tokens (140 to 163 us), the eight unpacking
-// warps on K and V alike (140 to 146 us). Unpackers of K and V apart: 144 to 139 us. Copies of codes
-// by half sectors: 207 us in the second case where whole ones took 140.
+// tensor memory (about 840 cycles of S, 700 of O a row tile and token tile), then come the hand-overs
+// between them and the softmax: 128 sequences x 8 heads of 4-bit codes x 4 query heads, prefix
+// 32,768, 146 us in all, 475 TFLOP/s (0.29 of the measured bf16 rate); this kernel 100 us, tensor pipe
+// 37 % busy while an SM works. One row tile: unpacking: 96 sequences x 32 heads of 8-bit codes, prefix
+// 8192, 131 us in all, this kernel 52 us. The rest of both is the sequences' own level, the merge
+// (about 9 us) and what lies between them. The keys' factors, read by every softmax thread for every
+// token, and the second reference cost about 10 us in the first case and 4 in the second, over images
+// that carried the scales.
+// Tried and slower (first case, while the images carried the scales): S in two halves of the tokens
+// (140 to 163 us), the eight unpacking warps on K and V alike (140 to 146 us). Unpackers of K and V
+// apart: 144 to 139 us. Copies of codes by half sectors: 207 us in the second case where whole ones
+// took 140. V's factor a token's as well as K's, for images of V without scales: 159 us and 128, where
+// a power of two per 32 tokens takes 149 and 127.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -63,7 +68,7 @@ constexpr int kThreads = 32 * (kDq0 + 2 * kDqWarps);
 constexpr float kNegInf = -INFINITY;
 // Registers a thread: what the block is launched with (65,536 over its threads), and what the four
 // warps in front give to the softmax groups' sixteen, whose 64 products a row and thread do not fit
-// otherwise (first case below: 153 us without, 148 with; 88 registers with less for unpacking 151).
+// otherwise (first case above: 153 us without, 148 with; 88 registers with less for unpacking 151).
 constexpr int kLaunchRegs = 72, kMmaRegs = 40, kSoftmaxRegs = 80;
 static_assert(kMmaRegs + 4 * kSoftmaxRegs + 2 * kLaunchRegs <= 7 * kLaunchRegs);
 
