@@ -378,7 +378,7 @@ __device__ __forceinline__ void weigh(const float (&x)[NT][4], const float (&rs)
   const bool beyond = attempt();
   if (__any_sync(0xffffffffu, beyond || special)) {
     look();
-    // only the rows that need a new reference take one: a row's result does not depend on the others'
+    // only the rows that need a new reference take one: a row's do not depend on the others'
     auto renew = [&](int nt, int k, float& m, float& M) {
       float y[2], z[2];
 #pragma unroll
